@@ -10,6 +10,12 @@ the calls raise.
     o, lse = A.attention(q, k, v, causal=True)        # q,k,v: CUDA bf16/fp16 [B,H,N,d]
     dq, dk, dv = A.attention_backward(q, k, v, o, do, lse, causal=True)
     o_new, lse_new = A.decode(q_new, k_cache, v_cache)
+
+A K/V cache of pages with a length per sequence:
+
+    cache = A.paged_cache(B, max_pages, n_pages, H_kv, page_size, d, dtype, device)
+    A.pages_append(cache, k_new, v_new)               # also pages_trim, _fork, _compact, _copy
+    o_new, lse_new = A.decode_paged(q_new, cache)
 """
 from __future__ import annotations
 
@@ -22,13 +28,15 @@ import torch
 __all__ = [
     "AttnError", "attention", "attention_from_host", "attn_fwd_raw", "attn_fwd_alibi_raw",
     "alibi_slopes", "decode", "decode_workspace_bytes", "attn_decode_raw",
-    "attn_decode_noalloc_raw", "attention_backward", "attn_bwd_raw", "bwd_workspace_bytes",
+    "attn_decode_noalloc_raw", "PagedCache", "paged_cache", "decode_paged",
+    "decode_paged_workspace_bytes", "pages_append", "pages_trim", "pages_fork", "pages_compact",
+    "pages_copy", "attention_backward", "attn_bwd_raw", "bwd_workspace_bytes",
     "unmasked_pairs",
     "visited_blocks", "fwd_unit_kind", "get_status", "set_watchdog_ns", "launch_count", "test_withhold_loads",
     "test_count_blocks", "test_force_units", "error_string",
     "library_path", "load_library", "EXPORTED_SYMBOLS", "ATTN_OK", "ATTN_ERR_INVALID_ARG",
     "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_MISALIGNED", "ATTN_ERR_CUDA", "ATTN_ERR_DEVICE_TIMEOUT",
-    "ATTN_BF16", "ATTN_FP16", "ATTN_OUT_F32",
+    "ATTN_ERR_NO_PAGES", "ATTN_BF16", "ATTN_FP16", "ATTN_OUT_F32",
 ]
 
 ATTN_OK = 0
@@ -37,6 +45,7 @@ ATTN_ERR_UNSUPPORTED = -2
 ATTN_ERR_MISALIGNED = -3
 ATTN_ERR_CUDA = -4
 ATTN_ERR_DEVICE_TIMEOUT = -5
+ATTN_ERR_NO_PAGES = -6
 ATTN_BF16 = 0
 ATTN_FP16 = 1
 ATTN_OUT_F32 = 0x10
@@ -47,7 +56,11 @@ EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_host", "attn_fwd_alibi", "attn_alibi_s
                     "attn_fwd_unit_kind",
                     "attn_get_status", "attn_set_watchdog_ns", "attn_launch_count",
                     "attn_test_withhold_loads", "attn_test_count_blocks", "attn_test_force_units",
-                    "attn_bwd", "attn_bwd_workspace_bytes")
+                    "attn_bwd", "attn_bwd_workspace_bytes",
+                    "attn_decode_paged", "attn_decode_paged_workspace_bytes",
+                    "attn_pages_append", "attn_pages_append_workspace_bytes", "attn_pages_trim",
+                    "attn_pages_fork", "attn_pages_compact", "attn_pages_compact_workspace_bytes",
+                    "attn_pages_copy")
 
 _LIB = None
 
@@ -110,6 +123,25 @@ def load_library():
     lib.attn_bwd.restype = ci
     lib.attn_bwd_workspace_bytes.argtypes = [ci] * 5
     lib.attn_bwd_workspace_bytes.restype = ctypes.c_longlong
+    ll = ctypes.c_longlong
+    lib.attn_decode_paged.argtypes = [vp, vp, vp, vp, vp, ci, vp, ll, ci, ci, ci, ci, ci, cf, ci, vp]
+    lib.attn_decode_paged.restype = ci
+    lib.attn_decode_paged_workspace_bytes.argtypes = [ci] * 6
+    lib.attn_decode_paged_workspace_bytes.restype = ll
+    lib.attn_pages_append.argtypes = [vp, vp, vp, vp, ci, vp, ll, vp]
+    lib.attn_pages_append.restype = ci
+    lib.attn_pages_append_workspace_bytes.argtypes = [ci] * 3
+    lib.attn_pages_append_workspace_bytes.restype = ll
+    lib.attn_pages_trim.argtypes = [vp, vp, vp, ci, vp]
+    lib.attn_pages_trim.restype = ci
+    lib.attn_pages_fork.argtypes = [vp, vp, vp, ci, vp]
+    lib.attn_pages_fork.restype = ci
+    lib.attn_pages_compact.argtypes = [vp, vp, vp, vp, vp, ll, vp]
+    lib.attn_pages_compact.restype = ci
+    lib.attn_pages_compact_workspace_bytes.argtypes = [ci]
+    lib.attn_pages_compact_workspace_bytes.restype = ll
+    lib.attn_pages_copy.argtypes = [vp, vp, vp, ci, vp]
+    lib.attn_pages_copy.restype = ci
     _LIB = lib
     return lib
 
@@ -189,6 +221,9 @@ def alibi_slopes(H: int, device=None) -> torch.Tensor:
 def default_scale(d: int) -> float:
     """1/sqrt(d) rounded once to float32 (the "HEAD_DIM ** -0.5" of the Hands-On guide)."""
     return float(torch.tensor(1.0 / math.sqrt(d), dtype=torch.float32))
+
+
+_DEFAULT_SCALE = {d: default_scale(d) for d in (64, 128)}
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -286,6 +321,267 @@ def decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = 
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode")
     return out, lse
+
+
+class _PagesStruct(ctypes.Structure):
+    """attn_pages_t of include/attn.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int) for n in ("n_pages", "H_kv", "page_size", "d", "B", "max_pages",
+                                            "dtype")]
+
+
+class PagedCache:
+    """A K/V cache made of pages (attn_pages_t): the handle that decode_paged()
+    and the pages_*() calls take.  It holds the tensors, checked once here, and
+    changes none of them itself.
+
+    k, v   [n_pages, H_kv, page_size, d] bf16/fp16
+    table  [B, max_pages] int32: page of each page_size positions of a sequence
+    lens   [B] int32: positions of each sequence
+    refs   [n_pages] int32: table entries that hold the page, 0 = free; None
+           for a cache that is only read by decode_paged()
+    All contiguous, on one device.  The tensors are read-only attributes: the
+    calls change their contents, in stream order.
+    """
+    __slots__ = ("_t", "_c", "_ptr")
+
+    def __init__(self, k, v, table, lens, refs=None):
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k, v must both be [n_pages, H_kv, page_size, d]")
+        if v.dtype != k.dtype:
+            raise TypeError("k and v must share one dtype")
+        code = _dtype_code(k)
+        if table.dim() != 2:
+            raise ValueError("table must be [B, max_pages]")
+        dev = k.device
+        _expect(k, "k", k.shape, k.dtype, dev)
+        _expect(v, "v", k.shape, k.dtype, dev)
+        _expect(table, "table", table.shape, torch.int32, dev)
+        _expect(lens, "lens", (table.shape[0],), torch.int32, dev)
+        if refs is not None:
+            _expect(refs, "refs", (k.shape[0],), torch.int32, dev)
+        self._t = (k, v, table, lens, refs)
+        self._c = _PagesStruct(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                               refs.data_ptr() if refs is not None else None, k.shape[0],
+                               k.shape[1], k.shape[2], k.shape[3], table.shape[0], table.shape[1],
+                               code)
+        self._ptr = ctypes.addressof(self._c)
+
+    k = property(lambda self: self._t[0])
+    v = property(lambda self: self._t[1])
+    table = property(lambda self: self._t[2])
+    lens = property(lambda self: self._t[3])
+    refs = property(lambda self: self._t[4])
+    device = property(lambda self: self._t[0].device)
+
+
+def paged_cache(B: int, max_pages: int, n_pages: int, H_kv: int, page_size: int, d: int,
+                dtype: torch.dtype = torch.bfloat16, device="cuda") -> PagedCache:
+    """An empty PagedCache: B empty sequences of up to max_pages pages each, every
+    page free.  The pages' contents are not initialised."""
+    k = torch.empty((n_pages, H_kv, page_size, d), dtype=dtype, device=device)
+    return PagedCache(k, torch.empty_like(k),
+                      torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                      torch.zeros(B, dtype=torch.int32, device=device),
+                      torch.zeros(n_pages, dtype=torch.int32, device=device))
+
+
+def decode_paged_workspace_bytes(B: int, H: int, H_kv: int, N_q: int, d: int,
+                                 shared_len: int = 0) -> int:
+    """Scratch bytes attn_decode_paged needs for these sizes (any lengths)."""
+    return int(load_library().attn_decode_paged_workspace_bytes(B, H, H_kv, N_q, d, shared_len))
+
+
+def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, window: int = 0,
+                 n_sink: int = 0, scale: float | None = None, shared_len: int = 0,
+                 shared_table: torch.Tensor | None = None, out_f32: bool = False,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 return_lse: bool = True, workspace: torch.Tensor | None = None):
+    """Attention of the new query rows q [B, H, N_q, d] against a paged cache
+    (attn_decode_paged).  Query row i of sequence b sits at position
+    lens[b] - N_q + i.  ``shared_len``, ``shared_table``: the batch's first
+    shared_len positions hold the same rows, in the pages that the int32 tensor
+    shared_table [ceil(shared_len / page_size)] lists; they are attended once for
+    the batch, with the same result.  ``workspace``: a CUDA uint8 tensor of at least
+    decode_paged_workspace_bytes(...) bytes; allocated here (torch) when
+    omitted.  Returns (o [B, H, N_q, d], lse [B, H, N_q] or None)."""
+    c = cache._c
+    if q.dim() != 4:
+        raise ValueError("q [B, H, N_q, d] expected")
+    B, H, N_q, d = q.shape
+    dev = q.device
+    if B != c.B or d != c.d:
+        raise ValueError(f"shape mismatch q={tuple(q.shape)}, cache of {c.B} sequences, d={c.d}")
+    if q.dtype != cache._t[0].dtype:
+        raise TypeError("q and the cache must share one dtype")
+    if dev != cache._t[0].device:
+        raise ValueError("q and the cache must be on one device")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    odt = torch.float32 if out_f32 else q.dtype
+    if out is not None:
+        _expect(out, "out", (B, H, N_q, d), odt, dev)
+    if lse is not None:
+        _expect(lse, "lse", (B, H, N_q), torch.float32, dev)
+    if shared_table is not None:
+        if shared_len < 0:
+            raise ValueError("shared_len must not be negative")
+        _expect(shared_table, "shared_table", (-(-shared_len // c.page_size),), torch.int32, dev)
+    if workspace is not None:
+        _expect_workspace(workspace, dev)
+    if not q.is_cuda:
+        raise ValueError("decode_paged() takes CUDA tensors")
+    if scale is None:
+        scale = _DEFAULT_SCALE.get(d) or default_scale(d)
+    if out is None:
+        out = torch.empty((B, H, N_q, d), dtype=odt, device=dev)
+    if lse is None and return_lse:
+        lse = torch.empty((B, H, N_q), dtype=torch.float32, device=dev)
+    lib = load_library()
+    if workspace is None:
+        need = lib.attn_decode_paged_workspace_bytes(B, H, c.H_kv, N_q, d, shared_len)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    with _Device(dev):
+        rc = lib.attn_decode_paged(q.data_ptr(), cache._ptr, out.data_ptr(),
+                                   lse.data_ptr() if lse is not None else None,
+                                   shared_table.data_ptr() if shared_table is not None else None,
+                                   shared_len, workspace.data_ptr() if workspace is not None else None,
+                                   workspace.numel() if workspace is not None else 0, H, N_q,
+                                   int(causal), window, n_sink, scale, int(out_f32), stream)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_paged")
+    return out, lse
+
+
+def _managed(cache: PagedCache, what: str, **ints):
+    """The device of a cache that a pages_*() call may change; checks that the
+    named tensors are contiguous 1-D int32 tensors there."""
+    if cache._t[4] is None:
+        raise ValueError(f"{what}() needs a cache with refs")
+    dev = cache._t[0].device
+    for name, t in ints.items():
+        if t is not None and (t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous()
+                              or t.device != dev):
+            raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on {dev}")
+    return dev
+
+
+def _on_cuda(dev, what: str):
+    if dev.type != "cuda":
+        raise ValueError(f"{what}() takes a CUDA cache")
+
+
+def _pages_call(dev, name: str, *args):
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    with _Device(dev):
+        rc = getattr(load_library(), name)(*args, stream)
+    if rc != ATTN_OK:
+        raise AttnError(rc, name)
+
+
+def _scratch(workspace, need: int, dev):
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    return workspace
+
+
+def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
+                 counts: torch.Tensor | None = None, *, workspace: torch.Tensor | None = None) -> None:
+    """Writes the first counts[b] (default: all) of the rows k_new, v_new
+    [B, H_kv, n_new, d] behind sequence b's last one (attn_pages_append): takes
+    the lowest free pages, copies a partly filled last page that other sequences
+    hold too, and updates table, lens and refs.  Sequences that the free pages
+    do not suffice for stay as they are; get_status() then gives
+    ATTN_ERR_NO_PAGES."""
+    c = cache._c
+    dev = _managed(cache, "pages_append", counts=counts)
+    n_new = k_new.shape[2] if k_new.dim() == 4 else -1
+    shape = (c.B, c.H_kv, n_new, c.d)
+    _expect(k_new, "k_new", shape, cache._t[0].dtype, dev)
+    _expect(v_new, "v_new", shape, cache._t[0].dtype, dev)
+    if counts is not None and counts.shape[0] != c.B:
+        raise ValueError(f"counts must have {c.B} elements")
+    if workspace is not None:
+        _expect_workspace(workspace, dev)
+    _on_cuda(dev, "pages_append")
+    workspace = _scratch(workspace, load_library().attn_pages_append_workspace_bytes(
+        c.B, n_new, c.page_size), dev)
+    _pages_call(dev, "attn_pages_append", cache._ptr, k_new.data_ptr(), v_new.data_ptr(),
+                counts.data_ptr() if counts is not None else None, n_new, workspace.data_ptr(),
+                workspace.numel())
+
+
+def pages_trim(cache: PagedCache, new_lens: torch.Tensor | None = None,
+               rows: torch.Tensor | None = None) -> None:
+    """Shortens sequences to at most new_lens[i] (default 0: frees them) and
+    releases the pages behind (attn_pages_trim).  ``rows``: int32 row numbers;
+    default rows 0, 1, ... (all of them when new_lens is None too)."""
+    c = cache._c
+    dev = _managed(cache, "pages_trim", new_lens=new_lens, rows=rows)
+    n = c.B
+    if rows is not None:
+        n = rows.shape[0]
+    elif new_lens is not None:
+        n = new_lens.shape[0]
+    if new_lens is not None and new_lens.shape[0] != n:
+        raise ValueError("new_lens and rows must be of one length")
+    if rows is None and n > c.B:
+        raise ValueError(f"new_lens has {n} elements for {c.B} sequences")
+    _on_cuda(dev, "pages_trim")
+    _pages_call(dev, "attn_pages_trim", cache._ptr, rows.data_ptr() if rows is not None else None,
+                new_lens.data_ptr() if new_lens is not None else None, n)
+
+
+def pages_fork(cache: PagedCache, parents: torch.Tensor, children: torch.Tensor) -> None:
+    """Makes the empty row children[i] a copy of row parents[i] that shares its
+    pages (attn_pages_fork); int32 tensors of one length."""
+    dev = _managed(cache, "pages_fork", parents=parents, children=children)
+    if parents.shape != children.shape:
+        raise ValueError("parents and children must be of one length")
+    _on_cuda(dev, "pages_fork")
+    _pages_call(dev, "attn_pages_fork", cache._ptr, parents.data_ptr(), children.data_ptr(),
+                parents.shape[0])
+
+
+def pages_compact(cache: PagedCache, *, table_out: torch.Tensor | None = None,
+                  refs_out: torch.Tensor | None = None, n_live: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Moves the live pages to the front of the cache (attn_pages_compact) and
+    renumbers the table and the counts, in place or into ``table_out`` and
+    ``refs_out``.  Returns the number of live pages as a one-element int32
+    tensor on the cache's device."""
+    c = cache._c
+    dev = _managed(cache, "pages_compact")
+    if table_out is not None:
+        _expect(table_out, "table_out", (c.B, c.max_pages), torch.int32, dev)
+    if refs_out is not None:
+        _expect(refs_out, "refs_out", (c.n_pages,), torch.int32, dev)
+    if n_live is not None:
+        _expect(n_live, "n_live", (1,), torch.int32, dev)
+    if workspace is not None:
+        _expect_workspace(workspace, dev)
+    _on_cuda(dev, "pages_compact")
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=dev)
+    workspace = _scratch(workspace, load_library().attn_pages_compact_workspace_bytes(c.n_pages), dev)
+    _pages_call(dev, "attn_pages_compact", cache._ptr,
+                table_out.data_ptr() if table_out is not None else None,
+                refs_out.data_ptr() if refs_out is not None else None, n_live.data_ptr(),
+                workspace.data_ptr(), workspace.numel())
+    return n_live
+
+
+def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copies page src[i]'s K and V rows to page dst[i] (attn_pages_copy); int32
+    tensors of one length, entries with src[i] < 0 are skipped."""
+    dev = _managed(cache, "pages_copy", src=src, dst=dst)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must be of one length")
+    _on_cuda(dev, "pages_copy")
+    _pages_call(dev, "attn_pages_copy", cache._ptr, src.data_ptr(), dst.data_ptr(), src.shape[0])
 
 
 def bwd_workspace_bytes(B: int, H: int, N: int, d: int, dtype: int) -> int:

@@ -1,7 +1,8 @@
 """Builds libattn.so in-tree with nvcc for sm_100a (B200).
 
-The library is five translation units (shared host code, the forward for
-d <= 64, the forward for d = 128, the backward, decode), compiled in parallel
+The library is seven translation units (shared host code, the forward for
+d <= 64, the forward for d = 128, the backward, decode, pages of a cache, decode over
+pages), compiled in parallel
 to objects under ``_objs/`` and linked into ``libattn.so``.
 
 Usage: python -m exact_tiled_attention_44_b200._build [--verbose]
@@ -17,9 +18,9 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-UNITS = ["attn_api.cu", "fwd_api.cu", "fwd_d128.cu", "bwd_api.cu", "decode_api.cu"]
+UNITS = ["attn_api.cu", "fwd_api.cu", "fwd_d128.cu", "bwd_api.cu", "decode_api.cu", "pages_api.cu", "paged_api.cu"]
 HEADERS = [os.path.join(CSRC, f) for f in ("host.h", "fwd_launch.cuh", "attn_kernel.cuh", "ptx.cuh", "bwd_kernel.cuh",
-                                           "decode_tc_kernel.cuh")] + [os.path.join(ROOT, "include", "attn.h")]
+                                           "decode_tc_kernel.cuh", "pages_kernel.cuh", "paged_kernel.cuh")] + [os.path.join(ROOT, "include", "attn.h")]
 DEPS = [os.path.join(CSRC, u) for u in UNITS] + HEADERS
 OUT = os.path.join(PKG, "libattn.so")
 OBJ_DIR = os.path.join(PKG, "_objs")

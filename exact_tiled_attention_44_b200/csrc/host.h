@@ -29,6 +29,7 @@ struct DeviceState {
   int* status = nullptr;           // device address of the status word
   uint64_t attr_set = 0;           // one bit per forward kernel instantiation
   uint32_t dec_attr_set = 0;       // one bit per decode kernel instantiation
+  uint32_t paged_attr_set = 0;     // one bit per paged decoding kernel instantiation
   uint32_t bwd_attr_set = 0;       // one bit per backward kernel instantiation
   // attn_fwd_host: two copy streams and the events that order its chunks,
   // created on its first call on the device and kept (guarded by g_host_mu)
@@ -54,6 +55,8 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 struct Sizes {
@@ -69,13 +72,16 @@ int validate(const void* q, const void* k, const void* v, const void* o, const f
              int B, int H, int H_kv, int N, int d, int causal, int window, int n_sink,
              float scale, int dtype, Sizes* sz, bool* empty);
 
+// Pure check of a paged cache's sizes, pointers and alignment (no CUDA API).
+int validate_pages(const attn_pages_t* c, bool need_refs);
+
 // State of the current device, initialised on first use (an sm_100 device is
 // required; anything else is ATTN_ERR_UNSUPPORTED).
 int device_state(DeviceState** out);
 
 // 3-D view [z][rows][d] of a contiguous [.., n, d] 16-bit tensor; box =
-// (min(d, 64), 128, 1) with the swizzle span equal to the box's row bytes.
-int encode_map(CUtensorMap* map, const void* base, bool bf16, int d, int n, int z);
+// (min(d, 64), rows, 1) with the swizzle span equal to the box's row bytes.
+int encode_map(CUtensorMap* map, const void* base, bool bf16, int d, int n, int z, int rows = 128);
 
 // Launches `kern` with programmatic stream serialisation: its CTAs may be
 // scheduled while the previous grid of the stream drains, run their set-up

@@ -1,0 +1,210 @@
+// paged_api.cu -- the decoding step over a K/V cache of pages:
+// attn_decode_paged and its workspace query.
+#include "host.h"
+#include "paged_kernel.cuh"
+
+namespace attn_host {
+
+namespace {
+
+// Ranges of the tile space (one CTA on each SM of a B200); fixed, so that the
+// workspace can be sized without a device.
+constexpr int kPagedRanges = 148;
+constexpr int kPagedMaxRows = 1024;   // (H / H_kv) * N_q
+
+// Workspace of one attending launch over `groups` groups: two slots a range
+// for the runs of split groups, and, behind or of a shared prefix, one result
+// for each group that a single run covers.
+struct PagedSpace {
+  size_t part_o, part_lse, own_o, own_lse, end;
+};
+
+PagedSpace paged_space(size_t at, size_t groups, int d) {
+  const size_t rows = size_t(2) * kPagedRanges * attn::PD_M, own = groups * attn::PD_M;
+  PagedSpace s;
+  s.part_o = at;
+  s.part_lse = s.part_o + rows * d * 4;
+  s.own_o = round_up(s.part_lse + rows * 4, 256);
+  s.own_lse = s.own_o + own * d * 4;
+  s.end = round_up(s.own_lse + own * 4, 256);
+  return s;
+}
+
+struct PagedPlan {
+  bool shared;
+  int row_tiles, prefix_tiles;   // row tiles of a sequence's, and of the batch's rows
+  PagedSpace own, prefix;
+  size_t bytes;
+};
+
+PagedPlan paged_plan(int B, int H, int H_kv, int N_q, int d, int shared_len) {
+  PagedPlan pl{};
+  const long long R = static_cast<long long>(H / H_kv) * N_q;
+  pl.shared = shared_len >= attn::PD_TILE;
+  pl.row_tiles = static_cast<int>((R + attn::PD_M - 1) / attn::PD_M);
+  pl.prefix_tiles = static_cast<int>((B * R + attn::PD_M - 1) / attn::PD_M);
+  const size_t groups = static_cast<size_t>(B) * H_kv * pl.row_tiles;
+  pl.own = paged_space(0, pl.shared ? groups : 0, d);
+  pl.bytes = pl.own.end;
+  if (pl.shared) {
+    pl.prefix = paged_space(pl.own.end, static_cast<size_t>(H_kv) * pl.prefix_tiles, d);
+    pl.bytes = pl.prefix.end;
+  }
+  return pl;
+}
+
+template <int D, bool BF16, bool F32>
+int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams* pre, const CUtensorMap& mk,
+                 const CUtensorMap& mv, cudaStream_t stream) {
+  auto kern = attn::attn_paged_kernel<D, BF16, F32>;
+  const int smem = attn::PdGeo<D>::SMEM_BYTES + 1024;
+  const uint32_t bit = 1u << ((D == 128 ? 4 : 0) + (BF16 ? 2 : 0) + (F32 ? 1 : 0));
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!(st->paged_attr_set & bit)) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+      st->paged_attr_set |= bit;
+    }
+  }
+  const auto done = [](cudaError_t e) {
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  };
+  int rc;
+  if (pre != nullptr) {
+    rc = done(launch_overlapped(kern, pre->ranges, attn::PD_THREADS, smem, stream, mk, mv, *pre));
+    if (rc != ATTN_OK) return rc;
+  }
+  rc = done(launch_overlapped(kern, dp.ranges, attn::PD_THREADS, smem, stream, mk, mv, dp));
+  if (rc != ATTN_OK) return rc;
+  if (pre != nullptr)
+    return done(launch_overlapped(attn::attn_paged_merge_shared<D, BF16, F32>, dp.B * dp.H_kv * dp.row_tiles,
+                                  attn::PD_THREADS, 0, stream, dp, *pre));
+  return done(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges, attn::PD_THREADS, 0, stream, dp));
+}
+
+}  // namespace
+
+}  // namespace attn_host
+
+using namespace attn_host;
+
+extern "C" {
+
+long long attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int N_q, int d, int shared_len) {
+  if (B < 0 || H < 0 || H_kv < 1 || N_q < 0 || d <= 0 || shared_len < 0) return -1;
+  if (B == 0 || H == 0 || N_q == 0) return 0;
+  if (H % H_kv != 0) return -1;
+  return static_cast<long long>(paged_plan(B, H, H_kv, N_q, d, shared_len).bytes);
+}
+
+int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse, const int* shared_table,
+                      int shared_len, void* workspace, long long workspace_bytes, int H, int N_q, int causal,
+                      int window, int n_sink, float scale, int out_f32, void* stream) {
+  int rc = validate_pages(kv, false);
+  if (rc != ATTN_OK) return rc;
+  if (H < 0 || N_q < 0 || shared_len < 0 || workspace_bytes < 0) return ATTN_ERR_INVALID_ARG;
+  if ((causal != 0 && causal != 1) || (out_f32 != 0 && out_f32 != 1)) return ATTN_ERR_INVALID_ARG;
+  if (window < 0 || n_sink < 0 || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (kv->B == 0 || H == 0 || N_q == 0) return ATTN_OK;
+  const int B = kv->B, H_kv = kv->H_kv, d = kv->d;
+  if (H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (window > 0 && !causal) return ATTN_ERR_UNSUPPORTED;
+  const long long R = static_cast<long long>(H / H_kv) * N_q;
+  if (R > kPagedMaxRows || static_cast<long long>(B) * H * N_q > INT32_MAX / 2) return ATTN_ERR_UNSUPPORTED;
+  if (kv->n_pages == 0) return ATTN_ERR_INVALID_ARG;
+  if (q == nullptr || o == nullptr || workspace == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (shared_len > 0 && shared_table == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || (lse != nullptr && !aligned16(lse)) ||
+      !aligned_to(workspace, 256) || !aligned_to(shared_table, 4))
+    return ATTN_ERR_MISALIGNED;
+  const PagedPlan pl = paged_plan(B, H, H_kv, N_q, d, shared_len);
+  if (static_cast<size_t>(workspace_bytes) < pl.bytes) return ATTN_ERR_INVALID_ARG;
+  // no output inside an input, the workspace or another output
+  const size_t rows = static_cast<size_t>(B) * H * N_q;
+  const size_t kv_bytes = static_cast<size_t>(kv->n_pages) * H_kv * kv->page_size * d * 2;
+  const struct { const void* p; size_t n; } out[3] = {
+      {o, rows * d * (out_f32 ? 4 : 2)}, {lse, lse != nullptr ? rows * 4 : 0}, {workspace, pl.bytes}};
+  const struct { const void* p; size_t n; } in[6] = {
+      {q, rows * d * 2}, {kv->k, kv_bytes}, {kv->v, kv_bytes},
+      {kv->table, static_cast<size_t>(B) * kv->max_pages * 4}, {kv->lens, static_cast<size_t>(B) * 4},
+      {shared_table, (static_cast<size_t>(shared_len) + kv->page_size - 1) / kv->page_size * 4}};
+  for (int i = 0; i < 3; ++i) {
+    if (out[i].n == 0) continue;
+    for (int j = 0; j < 6; ++j)
+      if (in[j].n != 0 && overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[j].n != 0 && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return ATTN_ERR_INVALID_ARG;
+  }
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  const bool bf16 = kv->dtype == ATTN_BF16;
+  alignas(64) CUtensorMap mk, mv;
+  const int z = kv->n_pages * H_kv;
+  if (encode_map(&mk, kv->k, bf16, d, kv->page_size, z, attn::PD_SLICE) != ATTN_OK ||
+      encode_map(&mv, kv->v, bf16, d, kv->page_size, z, attn::PD_SLICE) != ATTN_OK)
+    return ATTN_ERR_CUDA;
+  attn::PdParams dp{};
+  dp.q = q;
+  dp.o = o;
+  dp.lse = lse;
+  dp.table = kv->table;
+  dp.lens = kv->lens;
+  dp.status = st->status;
+  dp.watchdog_ns = g_watchdog_ns.load(std::memory_order_relaxed);
+  dp.B = B;
+  dp.H = H;
+  dp.H_kv = H_kv;
+  dp.N_q = N_q;
+  dp.n_pages = kv->n_pages;
+  dp.max_pages = kv->max_pages;
+  for (dp.page_shift = 4; (1 << dp.page_shift) < kv->page_size;) ++dp.page_shift;
+  dp.causal = causal;
+  const long long cap = static_cast<long long>(kv->max_pages) << dp.page_shift;
+  dp.window = window >= cap ? 0 : window;      // no row has that many positions before it
+  dp.n_sink = dp.window > 0 ? (n_sink < cap ? n_sink : static_cast<int>(cap)) : 0;
+  dp.scale_log2 = scale * 1.4426950408889634f;
+  dp.G = H / H_kv;
+  dp.R = static_cast<int>(R);
+  dp.row_tiles = pl.row_tiles;
+  dp.ranges = kPagedRanges;
+  dp.withhold_loads = take_withhold();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const auto place = [&](attn::PdParams& x, const PagedSpace& s) {
+    x.part_o = reinterpret_cast<float*>(ws + s.part_o);
+    x.part_lse = reinterpret_cast<float*>(ws + s.part_lse);
+    x.own_o = reinterpret_cast<float*>(ws + s.own_o);
+    x.own_lse = reinterpret_cast<float*>(ws + s.own_lse);
+  };
+  place(dp, pl.own);
+  attn::PdParams pre = dp;
+  // whole tiles of the prefix are attended once; a window moves with each
+  // row, so under one every sequence reads its own pages
+  const int shared_tiles = static_cast<int>((shared_len < cap ? shared_len : cap) / attn::PD_TILE);
+  const bool shared = shared_tiles > 0 && dp.window == 0;
+  if (shared) {
+    dp.shared_tiles = shared_tiles;
+    pre.shared_tiles = dp.shared_tiles;
+    pre.prefix = 1;
+    pre.table = shared_table;
+    pre.row_tiles = pl.prefix_tiles;
+    place(pre, pl.prefix);
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const attn::PdParams* pp = shared ? &pre : nullptr;
+  if (d == 128) {
+    if (bf16) return out_f32 ? launch_paged<128, true, true>(st, dp, pp, mk, mv, s)
+                             : launch_paged<128, true, false>(st, dp, pp, mk, mv, s);
+    return out_f32 ? launch_paged<128, false, true>(st, dp, pp, mk, mv, s)
+                   : launch_paged<128, false, false>(st, dp, pp, mk, mv, s);
+  }
+  if (bf16) return out_f32 ? launch_paged<64, true, true>(st, dp, pp, mk, mv, s)
+                           : launch_paged<64, true, false>(st, dp, pp, mk, mv, s);
+  return out_f32 ? launch_paged<64, false, true>(st, dp, pp, mk, mv, s)
+                 : launch_paged<64, false, false>(st, dp, pp, mk, mv, s);
+}
+
+}  // extern "C"

@@ -1,7 +1,9 @@
 /*
  * attn.h -- C ABI of the exact tiled attention library (libattn.so): the
- * forward (attn_fwd, attn_fwd_alibi, attn_fwd_host), its backward (attn_bwd) and
- * the split-KV decoding step (attn_decode, attn_decode_noalloc).
+ * forward (attn_fwd, attn_fwd_alibi, attn_fwd_host), its backward (attn_bwd),
+ * the split-KV decoding step (attn_decode, attn_decode_noalloc), and a K/V cache
+ * of pages: the decoding step over it (attn_decode_paged) and its management
+ * (attn_pages_append, _trim, _fork, _compact, _copy).
  *
  * The library computes, for every batch b and query head h,
  *
@@ -62,7 +64,8 @@ typedef enum {
   ATTN_ERR_UNSUPPORTED = -2,     /* valid request this library does not handle */
   ATTN_ERR_MISALIGNED = -3,      /* a tensor pointer is not 16-byte aligned    */
   ATTN_ERR_CUDA = -4,            /* a CUDA runtime/driver call failed          */
-  ATTN_ERR_DEVICE_TIMEOUT = -5   /* a kernel wait exceeded its time limit      */
+  ATTN_ERR_DEVICE_TIMEOUT = -5,  /* a kernel wait exceeded its time limit      */
+  ATTN_ERR_NO_PAGES = -6         /* too few free pages (attn_pages_append)     */
 } attn_status_t;
 
 /* dtype argument: element type of q, k, v (and o), optionally OR-ed with
@@ -216,6 +219,166 @@ long long attn_decode_workspace_bytes(int B, int H, int H_kv, int N_q, int N_kv,
 int attn_decode_noalloc(const void* q, const void* k, const void* v, void* o, float* lse,
                         int B, int H, int H_kv, int N_q, int N_kv, int d, int causal,
                         int window, int n_sink, float scale, int dtype, void* stream);
+
+/*
+ * attn_pages_t -- a K/V cache made of pages, shared by every attn_pages_*
+ * call and by attn_decode_paged (the pages have no counterpart; "USAAIO Lesson
+ * 91", slide 31, is why it is there: every decoding step re-reads the whole
+ * K/V cache, which therefore has to be kept and shared).
+ *
+ *   k, v     device, [n_pages, H_kv, page_size, d], 16-byte aligned, 16-bit
+ *   table    device, [B, max_pages] int32: position j of sequence b lies in
+ *            page table[b][j / page_size], row j % page_size.  Entries past a
+ *            sequence's pages are not read by attention (attn_pages_trim and
+ *            attn_pages_fork set them to -1).
+ *   lens     device, [B] int32: positions of each sequence (0: none)
+ *   refs     device, [n_pages] int32: how many table entries hold the page;
+ *            0 = free.  attn_decode_paged does not read it (NULL is allowed
+ *            there).
+ *   page_size  16, 32, 64, 128 or 256 (else ATTN_ERR_UNSUPPORTED)
+ *   d        16, 32, 64 or 128 (attn_decode_paged: 64 or 128)
+ *   dtype    ATTN_BF16 or ATTN_FP16 (a flag bit is ATTN_ERR_INVALID_ARG)
+ *   B, n_pages, max_pages >= 0, H_kv >= 1; n_pages * H_kv < 2^31 and
+ *            max_pages * page_size <= 2^30 (else ATTN_ERR_UNSUPPORTED)
+ *
+ * The struct is read during the call only.  Tables, lengths and counts are
+ * device data that no call can check on the host.  What cannot be right is
+ * never followed: a page number outside [0, n_pages), a length outside
+ * [0, max_pages * page_size], a row outside [0, B) or a count outside its
+ * range leaves the entry it stands in undone, and ATTN_ERR_INVALID_ARG is
+ * recorded in the device status word (attn_get_status).  The calls change
+ * table, lens and refs in stream order; they are deterministic, may be
+ * captured into a graph, and must not overlap calls on the same cache.
+ */
+typedef struct attn_pages {
+  void* k;
+  void* v;
+  int* table;
+  int* lens;
+  int* refs;
+  int n_pages, H_kv, page_size, d, B, max_pages, dtype;
+} attn_pages_t;
+
+/*
+ * attn_decode_paged -- attn_decode against a cache of pages, with a length per
+ * sequence and, optionally, a prefix that the batch shares.
+ *
+ *   q      device, [B, H, N_q, d], B, d and dtype those of `kv`; query row i of
+ *          sequence b sits at position lens[b] - N_q + i
+ *   o      device, [B, H, N_q, d] (16-bit, or float32 when out_f32 is 1)
+ *   lse    device, [B, H, N_q] float32, or NULL
+ *   shared_table, shared_len   the first min(shared_len, lens[b]) positions of
+ *          every sequence hold the same rows, and shared_table (device,
+ *          [ceil(shared_len / page_size)] int32) lists pages that hold them.
+ *          Whole 128-position tiles of them are then attended once for the query rows
+ *          of all sequences instead of once a sequence.  It changes what is
+ *          read, not what is computed: the result is that of shared_len = 0,
+ *          up to rounding.  0 and NULL: nothing is shared.  With window > 0
+ *          every sequence reads its own pages.  `table` lists all of a
+ *          sequence's pages, the shared ones too.
+ *   workspace, workspace_bytes   device scratch of at least
+ *          attn_decode_paged_workspace_bytes(...) bytes, 256-byte aligned;
+ *          needs no initial contents, not to be shared by calls in flight at
+ *          once
+ *   N_q >= 0; (H / H_kv) * N_q <= 1024 (else ATTN_ERR_UNSUPPORTED); d is 64 or
+ *   128; causal, window, n_sink, scale as for attn_fwd
+ *
+ * A query row keeps key j iff j < lens[b] and the mask rule of attn_fwd holds
+ * with the row's position for i.  A row that keeps nothing (an empty sequence,
+ * or a row before position 0 under causal) gets O = 0 and LSE = -inf.  Rows of
+ * the cache that no query row of the sequence keeps are never used, whatever
+ * they hold; a non-finite V row that some query row keeps may also reach the other
+ * rows of the same sequence and K/V head.  A page number outside [0, n_pages)
+ * reads as rows of zeros, and a length past the table's counts as the table's; both
+ * record ATTN_ERR_INVALID_ARG in the status word.  Deterministic: equal inputs
+ * give bitwise-equal outputs.
+ */
+int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse,
+                      const int* shared_table, int shared_len, void* workspace,
+                      long long workspace_bytes, int H, int N_q, int causal, int window, int n_sink,
+                      float scale, int out_f32, void* stream);
+
+/* Host only: bytes of workspace attn_decode_paged needs for these sizes (it
+ * depends neither on the device, the lengths nor the mask), 0 for an empty
+ * problem, -1 for invalid sizes. */
+long long attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int N_q, int d, int shared_len);
+
+/*
+ * attn_pages_append -- writes new rows behind each sequence's last one.
+ *
+ *   k_new, v_new  device, [B, H_kv, n_new, d], the cache's type, 16-byte aligned
+ *   counts        device, [B] int32, or NULL: the first counts[b] (NULL: all
+ *                 n_new) rows of sequence b are appended, 0 <= counts[b] <= n_new
+ *   workspace     at least attn_pages_append_workspace_bytes(B, n_new, page_size)
+ *                 bytes, 16-byte aligned, needs no initial contents
+ *
+ * Pages come from the free ones (refs == 0): in order of the sequences, the
+ * lowest first.  A sequence whose last page is partly filled and held by others
+ * too (refs > 1) gets a page with a copy of its rows first (copy on write; the
+ * old page loses a reference).  When the free pages do not suffice, the first
+ * sequence that cannot be served and every later one that needs a page stay
+ * as they are, and ATTN_ERR_NO_PAGES is recorded in the status word.  Two
+ * launches: the decisions, then the rows.
+ */
+int attn_pages_append(const attn_pages_t* cache, const void* k_new, const void* v_new,
+                      const int* counts, int n_new, void* workspace, long long workspace_bytes,
+                      void* stream);
+
+/* Host only: workspace bytes of attn_pages_append (-1: invalid sizes). */
+long long attn_pages_append_workspace_bytes(int B, int n_new, int page_size);
+
+/*
+ * attn_pages_trim -- shortens sequences and releases the pages behind them:
+ * for each listed row, lens = min(lens, new_lens), and the table entries past
+ * the last kept page lose their reference and become -1.  Length 0 frees the
+ * sequence.
+ *   rows      device, [n] int32, or NULL for rows 0 .. n - 1; a row listed twice
+ *             ends at its smallest length
+ *   new_lens  device, [n] int32 >= 0, or NULL for 0
+ */
+int attn_pages_trim(const attn_pages_t* cache, const int* rows, const int* new_lens, int n,
+                    void* stream);
+
+/*
+ * attn_pages_fork -- makes row children[i] a copy of row parents[i] that shares
+ * its pages (each gains a reference; no row of K or V moves).
+ *   parents, children  device, [n] int32
+ * A child must be empty (lens == 0), listed once, and listed as no parent; a
+ * fork that breaks this is skipped (of two with one child, the first is done) and
+ * records ATTN_ERR_INVALID_ARG.
+ */
+int attn_pages_fork(const attn_pages_t* cache, const int* parents, const int* children, int n,
+                    void* stream);
+
+/*
+ * attn_pages_compact -- moves the live pages (refs > 0) to the front of the
+ * cache: with n of them, the k-th live page at or past index n moves to the
+ * k-th free index below n, the fewest moves there are.
+ *   table_out  device, [B, max_pages] int32: the table with the new page
+ *              numbers; NULL (or cache->table): in place
+ *   refs_out   device, [n_pages] int32: the counts of the moved pages; NULL
+ *              (or cache->refs): in place
+ *   n_live     device, [1] int32: n, or NULL
+ *   workspace  at least attn_pages_compact_workspace_bytes(n_pages) bytes,
+ *              16-byte aligned, needs no initial contents
+ * The rows a moved page had stay readable at its old place until that is
+ * handed out again, so work in flight on the old table is not disturbed when
+ * table_out is a second table.  Two launches.
+ */
+int attn_pages_compact(const attn_pages_t* cache, int* table_out, int* refs_out, int* n_live,
+                       void* workspace, long long workspace_bytes, void* stream);
+
+/* Host only: workspace bytes of attn_pages_compact (-1: invalid sizes). */
+long long attn_pages_compact_workspace_bytes(int n_pages);
+
+/*
+ * attn_pages_copy -- copies the K and V rows of page src[i] to page dst[i], for
+ * every K/V head.  src, dst: device, [n] int32; an entry with src[i] < 0 is
+ * skipped.  No page may be the source of one entry and the destination of another,
+ * nor the destination of two (its contents are then unspecified).  Table, lens
+ * and refs are neither read nor written.
+ */
+int attn_pages_copy(const attn_pages_t* cache, const int* src, const int* dst, int n, void* stream);
 
 /*
  * attn_bwd -- gradients dQ, dK, dV of attn_fwd's output O for an upstream
