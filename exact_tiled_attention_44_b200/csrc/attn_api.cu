@@ -105,15 +105,15 @@ int device_state(DeviceState** out) {
   return ATTN_OK;
 }
 
-// 3-D view [z][rows][d] of a contiguous [.., N, d] tensor; box = (cw, rows, 1)
+// 3-D view [z][rows][d] of a contiguous [.., N, d] tensor; box = (cw, 128, 1)
 // with the swizzle span equal to the box's row bytes.
-int encode_map(CUtensorMap* map, const void* base, bool bf16, int d, int n, int z, int rows) {
+int encode_map(CUtensorMap* map, const void* base, bool bf16, int d, int n, int z) {
   const int cw = d < 64 ? d : 64;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n),
                               static_cast<cuuint64_t>(z)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
                                  static_cast<cuuint64_t>(n) * d * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(cw), static_cast<cuuint32_t>(rows), 1u};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(cw), 128u, 1u};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUtensorMapSwizzle sw = cw * 2 == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                 : cw * 2 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B

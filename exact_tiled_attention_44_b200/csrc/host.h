@@ -80,8 +80,8 @@ int validate_pages(const attn_pages_t* c, bool need_refs);
 int device_state(DeviceState** out);
 
 // 3-D view [z][rows][d] of a contiguous [.., n, d] 16-bit tensor; box =
-// (min(d, 64), rows, 1) with the swizzle span equal to the box's row bytes.
-int encode_map(CUtensorMap* map, const void* base, bool bf16, int d, int n, int z, int rows = 128);
+// (min(d, 64), 128, 1) with the swizzle span equal to the box's row bytes.
+int encode_map(CUtensorMap* map, const void* base, bool bf16, int d, int n, int z);
 
 // Launches `kern` with programmatic stream serialisation: its CTAs may be
 // scheduled while the previous grid of the stream drains, run their set-up

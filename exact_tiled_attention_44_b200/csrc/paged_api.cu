@@ -7,9 +7,9 @@ namespace attn_host {
 
 namespace {
 
-// Ranges of the tile space (one CTA on each SM of a B200); fixed, so that the
+// Ranges of the tile space (two CTAs on each SM of a B200); fixed, so that the
 // workspace can be sized without a device.
-constexpr int kPagedRanges = 148;
+constexpr int kPagedRanges = 296;
 constexpr int kPagedMaxRows = 1024;   // (H / H_kv) * N_q
 
 // Workspace of one attending launch over `groups` groups: two slots a range
@@ -19,8 +19,8 @@ struct PagedSpace {
   size_t part_o, part_lse, own_o, own_lse, end;
 };
 
-PagedSpace paged_space(size_t at, size_t groups, int d) {
-  const size_t rows = size_t(2) * kPagedRanges * attn::PD_M, own = groups * attn::PD_M;
+PagedSpace paged_space(size_t at, size_t groups, int m, int d) {
+  const size_t rows = size_t(2) * kPagedRanges * m, own = groups * m;
   PagedSpace s;
   s.part_o = at;
   s.part_lse = s.part_o + rows * d * 4;
@@ -32,7 +32,8 @@ PagedSpace paged_space(size_t at, size_t groups, int d) {
 
 struct PagedPlan {
   bool shared;
-  int row_tiles, prefix_tiles;   // row tiles of a sequence's, and of the batch's rows
+  int m, row_tiles;                // rows of a group, and groups of a sequence's rows
+  int prefix_m, prefix_tiles;      // the same of the batch's rows
   PagedSpace own, prefix;
   size_t bytes;
 };
@@ -41,24 +42,47 @@ PagedPlan paged_plan(int B, int H, int H_kv, int N_q, int d, int shared_len) {
   PagedPlan pl{};
   const long long R = static_cast<long long>(H / H_kv) * N_q;
   pl.shared = shared_len >= attn::PD_TILE;
-  pl.row_tiles = static_cast<int>((R + attn::PD_M - 1) / attn::PD_M);
-  pl.prefix_tiles = static_cast<int>((B * R + attn::PD_M - 1) / attn::PD_M);
+  pl.m = R <= 8 ? 8 : 16;
+  pl.row_tiles = static_cast<int>((R + pl.m - 1) / pl.m);
+  pl.prefix_m = B * R <= 8 ? 8 : 16;
+  pl.prefix_tiles = static_cast<int>((B * R + pl.prefix_m - 1) / pl.prefix_m);
   const size_t groups = static_cast<size_t>(B) * H_kv * pl.row_tiles;
-  pl.own = paged_space(0, pl.shared ? groups : 0, d);
+  pl.own = paged_space(0, pl.shared ? groups : 0, pl.m, d);
   pl.bytes = pl.own.end;
   if (pl.shared) {
-    pl.prefix = paged_space(pl.own.end, static_cast<size_t>(H_kv) * pl.prefix_tiles, d);
+    pl.prefix = paged_space(pl.own.end, static_cast<size_t>(H_kv) * pl.prefix_tiles, pl.prefix_m, d);
     pl.bytes = pl.prefix.end;
   }
   return pl;
 }
 
-template <int D, bool BF16, bool F32>
-int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams* pre, const CUtensorMap& mk,
-                 const CUtensorMap& mv, cudaStream_t stream) {
-  auto kern = attn::attn_paged_kernel<D, BF16, F32>;
-  const int smem = attn::PdGeo<D>::SMEM_BYTES + 1024;
-  const uint32_t bit = 1u << ((D == 128 ? 4 : 0) + (BF16 ? 2 : 0) + (F32 ? 1 : 0));
+// 4-D view [z][d / 64][page_size][64] of the pages of one K/V head each (z =
+// page * H_kv + head); one box is a slice of PD_SLICE rows, its 64-column
+// chunks one behind the other, in the 128-byte swizzle.
+int encode_pages(CUtensorMap* map, const void* base, bool bf16, int d, int page_size, int z) {
+  const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(d / 64),
+                              static_cast<cuuint64_t>(z)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, 128u, static_cast<cuuint64_t>(page_size) * d * 2};
+  const cuuint32_t box[4] = {64u, attn::PD_SLICE, static_cast<cuuint32_t>(d / 64), 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int counted(cudaError_t e) {
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D, int NT, bool BF16, bool F32>
+int launch_attend(DeviceState* st, const attn::PdParams& dp, const CUtensorMap& mk, const CUtensorMap& mv,
+                  cudaStream_t stream) {
+  auto kern = attn::attn_paged_kernel<D, NT, BF16, F32>;
+  const int smem = attn::PdGeo<D, NT>::SMEM_BYTES + 1024;
+  const uint32_t bit = 1u << ((D == 128 ? 8 : 0) + (NT == 2 ? 4 : 0) + (BF16 ? 2 : 0) + (F32 ? 1 : 0));
   {
     std::lock_guard<std::mutex> lock(g_mu);
     if (!(st->paged_attr_set & bit)) {
@@ -67,21 +91,24 @@ int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams
       st->paged_attr_set |= bit;
     }
   }
-  const auto done = [](cudaError_t e) {
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return counted(launch_overlapped(kern, dp.ranges, attn::PD_THREADS, smem, stream, mk, mv, dp));
+}
+
+template <int D, bool BF16, bool F32>
+int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams* pre, const CUtensorMap& mk,
+                 const CUtensorMap& mv, cudaStream_t stream) {
+  const auto attend = [&](const attn::PdParams& x) {
+    return x.m == 8 ? launch_attend<D, 1, BF16, F32>(st, x, mk, mv, stream)
+                    : launch_attend<D, 2, BF16, F32>(st, x, mk, mv, stream);
   };
-  int rc;
-  if (pre != nullptr) {
-    rc = done(launch_overlapped(kern, pre->ranges, attn::PD_THREADS, smem, stream, mk, mv, *pre));
-    if (rc != ATTN_OK) return rc;
-  }
-  rc = done(launch_overlapped(kern, dp.ranges, attn::PD_THREADS, smem, stream, mk, mv, dp));
+  int rc = ATTN_OK;
+  if (pre != nullptr) rc = attend(*pre);
+  if (rc == ATTN_OK) rc = attend(dp);
   if (rc != ATTN_OK) return rc;
   if (pre != nullptr)
-    return done(launch_overlapped(attn::attn_paged_merge_shared<D, BF16, F32>, dp.B * dp.H_kv * dp.row_tiles,
-                                  attn::PD_THREADS, 0, stream, dp, *pre));
-  return done(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges, attn::PD_THREADS, 0, stream, dp));
+    return counted(launch_overlapped(attn::attn_paged_merge_shared<D, BF16, F32>, dp.B * dp.H_kv * dp.row_tiles,
+                                     attn::PD_THREADS, 0, stream, dp, *pre));
+  return counted(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges, attn::PD_THREADS, 0, stream, dp));
 }
 
 }  // namespace
@@ -114,6 +141,10 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   if (window > 0 && !causal) return ATTN_ERR_UNSUPPORTED;
   const long long R = static_cast<long long>(H / H_kv) * N_q;
   if (R > kPagedMaxRows || static_cast<long long>(B) * H * N_q > INT32_MAX / 2) return ATTN_ERR_UNSUPPORTED;
+  // the tiles of all groups are counted in 32 bits
+  const long long most = static_cast<long long>(kv->max_pages) * kv->page_size;
+  const long long tile_groups = (R + 15) / 16 * B * H_kv;
+  if ((most + attn::PD_TILE) / attn::PD_TILE * tile_groups > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
   if (kv->n_pages == 0) return ATTN_ERR_INVALID_ARG;
   if (q == nullptr || o == nullptr || workspace == nullptr) return ATTN_ERR_INVALID_ARG;
   if (shared_len > 0 && shared_table == nullptr) return ATTN_ERR_INVALID_ARG;
@@ -144,8 +175,8 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   const bool bf16 = kv->dtype == ATTN_BF16;
   alignas(64) CUtensorMap mk, mv;
   const int z = kv->n_pages * H_kv;
-  if (encode_map(&mk, kv->k, bf16, d, kv->page_size, z, attn::PD_SLICE) != ATTN_OK ||
-      encode_map(&mv, kv->v, bf16, d, kv->page_size, z, attn::PD_SLICE) != ATTN_OK)
+  if (encode_pages(&mk, kv->k, bf16, d, kv->page_size, z) != ATTN_OK ||
+      encode_pages(&mv, kv->v, bf16, d, kv->page_size, z) != ATTN_OK)
     return ATTN_ERR_CUDA;
   attn::PdParams dp{};
   dp.q = q;
@@ -169,6 +200,7 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   dp.scale_log2 = scale * 1.4426950408889634f;
   dp.G = H / H_kv;
   dp.R = static_cast<int>(R);
+  dp.m = pl.m;
   dp.row_tiles = pl.row_tiles;
   dp.ranges = kPagedRanges;
   dp.withhold_loads = take_withhold();
@@ -190,6 +222,7 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
     pre.shared_tiles = dp.shared_tiles;
     pre.prefix = 1;
     pre.table = shared_table;
+    pre.m = pl.prefix_m;
     pre.row_tiles = pl.prefix_tiles;
     place(pre, pl.prefix);
   }

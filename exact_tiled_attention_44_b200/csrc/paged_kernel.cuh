@@ -9,8 +9,8 @@
 //
 // Work split ("Building a FlashAttention-style tiled self-attention block in
 // pure NumPy", "Extending It", item 6: split the sequence, then reduce the
-// partial outputs): a group is one sequence, one K/V head and up to PD_M of
-// its (H / H_kv) * N_q query rows.  The kept 128-position tiles of all groups
+// partial outputs): a group is one sequence, one K/V head and up to m of
+// its (H / H_kv) * N_q query rows.  The kept 64-position tiles of all groups
 // are laid end to end, by the lengths on the device, and cut into equal
 // ranges, one for each CTA, so ragged lengths leave no CTA idle.  The part of
 // a range inside one group is a run.  A group covered by one run is written
@@ -27,20 +27,20 @@
 
 namespace attn {
 
-constexpr int PD_TILE = 128;            // positions of a tile
+constexpr int PD_TILE = 64;             // positions of a tile
 constexpr int PD_SLICE = 16;            // positions a warp loads and attends at a time
 constexpr int PD_WARPS = PD_TILE / PD_SLICE;
 constexpr int PD_THREADS = 32 * PD_WARPS;
-constexpr int PD_M = 16;                // query rows of a group
+constexpr int PD_LENS = 512;            // lengths kept in shared memory
 
 struct PdParams {
   const void* q;
   void* o;
   float* lse;
-  float* part_o;        // [2 * gridDim.x][PD_M][D] results of runs of split groups
-  float* part_lse;      // [2 * gridDim.x][PD_M]
-  float* own_o;         // with a shared prefix: [groups][PD_M][D] results of groups with one run
-  float* own_lse;       // [groups][PD_M]
+  float* part_o;        // [2 * gridDim.x][m][D] results of runs of split groups
+  float* part_lse;      // [2 * gridDim.x][m]
+  float* own_o;         // with a shared prefix: [groups][m][D] results of groups with one run
+  float* own_lse;       // [groups][m]
   const int* table;     // [B][max_pages], or the shared table
   const int* lens;
   int* status;
@@ -51,6 +51,7 @@ struct PdParams {
   float scale_log2;     // scale * log2(e)
   int G;                // H / H_kv
   int R;                // G * N_q query rows of a sequence and K/V head
+  int m;                // query rows of a group: 8 or 16
   int row_tiles;        // groups of a sequence and K/V head (prefix: of a K/V head)
   int shared_tiles;     // whole tiles of the shared prefix
   int prefix;           // this launch attends the shared prefix
@@ -58,36 +59,49 @@ struct PdParams {
   int withhold_loads;   // test hook: no slice is loaded, so every wait runs out
 };
 
-// Shared memory of head dimension D: a ring of PD_NST slices (K, then V) for
-// each warp, the exchange buffer of the epilogue, row statistics, barriers.
-template <int D>
+// Shared memory of head dimension D and 8 NT rows a group: a ring of NST
+// slices (K, then V) for each warp, the exchange buffer of the epilogue, row
+// statistics, a run's query rows, the first sequences' lengths, barriers.
+template <int D, int NT>
 struct PdGeo {
   static_assert(D == 64 || D == 128, "the paged decoding kernel supports d = 64 and 128");
-  static constexpr int NST = D == 128 ? 3 : 5;
+  static constexpr int M = 8 * NT;
+  static constexpr int NST = D == 128 ? 3 : 6;
   static constexpr int NCH = D / 64;                    // 64-column chunks, 128-byte swizzle
   static constexpr int CHUNK_BYTES = PD_SLICE * 128;
   static constexpr int HALF_BYTES = NCH * CHUNK_BYTES;  // K (or V) of a slice
   static constexpr int STAGE_BYTES = 2 * HALF_BYTES;
   static constexpr int RING_BYTES = PD_WARPS * NST * STAGE_BYTES;
-  static constexpr int X_OFF = RING_BYTES;              // [PD_WARPS][PD_M][64] float
-  static constexpr int STAT_OFF = X_OFF + PD_WARPS * PD_M * 64 * 4;
-  static constexpr int BAR_OFF = STAT_OFF + 3 * PD_WARPS * PD_M * 4;
-  static constexpr int SCAN_OFF = BAR_OFF + PD_WARPS * NST * 8;   // long long [PD_WARPS + 2]
-  static constexpr int ABORT_OFF = SCAN_OFF + (PD_WARPS + 2) * 8;
+  static constexpr int Q_CHUNK = M * 128;               // the query rows in the same chunks
+  static constexpr int Q_OFF = RING_BYTES;
+  static constexpr int Q_VECS = M * D / 8;              // 16-byte vectors of the rows
+  static constexpr int X_ROWS = 512 / D;                // rows combined at a time
+  static constexpr int X_LD = D + 4;                    // floats from row to row
+  static constexpr int X_OFF = Q_OFF + NCH * Q_CHUNK;   // float [PD_WARPS][X_ROWS][X_LD]
+  static constexpr int STAT_OFF = X_OFF + PD_WARPS * X_ROWS * X_LD * 4;   // float [3][PD_WARPS][M]
+  static constexpr int LENS_OFF = STAT_OFF + 3 * PD_WARPS * M * 4;
+  static constexpr int BAR_OFF = LENS_OFF + PD_LENS * 4;
+  static constexpr int SCAN_OFF = BAR_OFF + PD_WARPS * NST * 8;   // int [PD_WARPS + 2]
+  static constexpr int ABORT_OFF = SCAN_OFF + (PD_WARPS + 2) * 4;
   static constexpr int SMEM_BYTES = ABORT_OFF + 8;
-  static_assert(SMEM_BYTES + 1024 <= 232448, "shared memory budget");
+  // two CTAs on an SM
+  static_assert(2 * (SMEM_BYTES + 2048) <= 233472, "shared memory budget");
 };
 
 // ------------------------------------------------------------ work split
 
-// The positions a sequence's rows may keep: [0, 128 sb) and [128 w0, len).
+// The positions a sequence's rows may keep: tiles [0, sb) and [w0, ...) of len.
 struct PdSeq {
   int len;      // positions (clamped to the table)
   int sb, w0;   // tiles [0, sb), then [w0, ...)
   int tiles;    // at least 1, so that every group has a run
 };
 
-__device__ __forceinline__ PdSeq pd_seq(const PdParams& p, int b) {
+__device__ __forceinline__ int pd_len_of(const PdParams& p, int b) {
+  return min(max(p.lens[b], 0), p.max_pages << p.page_shift);
+}
+
+__device__ __forceinline__ PdSeq pd_seq(const PdParams& p, int len) {
   PdSeq s;
   if (p.prefix) {
     s.len = p.shared_tiles * PD_TILE;
@@ -96,130 +110,182 @@ __device__ __forceinline__ PdSeq pd_seq(const PdParams& p, int b) {
     s.tiles = p.shared_tiles;
     return s;
   }
-  const int cap = p.max_pages << p.page_shift;
-  s.len = min(max(p.lens[b], 0), cap);
-  const int nt = (s.len + PD_TILE - 1) / PD_TILE;
+  s.len = len;
+  const int nt = (len + PD_TILE - 1) / PD_TILE;
   s.sb = 0;
   s.w0 = p.shared_tiles;
   if (p.window > 0) {
-    const long long first = static_cast<long long>(s.len) - p.N_q - p.window + 1;
-    s.sb = min((min(p.n_sink, s.len) + PD_TILE - 1) / PD_TILE, nt);
-    s.w0 = max(first > 0 ? static_cast<int>(first) / PD_TILE : 0, s.sb);
+    const int first = len - p.N_q - p.window + 1;      // both below 2^30 + 1024
+    s.sb = min((min(p.n_sink, len) + PD_TILE - 1) / PD_TILE, nt);
+    s.w0 = max(first > 0 ? first / PD_TILE : 0, s.sb);
   }
   s.tiles = max(1, s.sb + max(0, nt - s.w0));
   return s;
 }
 
-__host__ __device__ inline long long pd_start(long long c, long long F, int grid) { return c * F / grid; }
+// F tiles in `n` ranges: the first `more` ranges have one tile more than the
+// other `each`.
+struct PdCut {
+  int n, each, more;
+};
 
-// The range that holds flattened tile f.
-__host__ __device__ inline int pd_range_of(long long f, long long F, int grid) {
-  int c = static_cast<int>(f * grid / F);
-  while (c + 1 < grid && pd_start(c + 1, F, grid) <= f) ++c;
-  while (c > 0 && pd_start(c, F, grid) > f) --c;
+__device__ __forceinline__ PdCut pd_cut(int F, int n) {
+  PdCut c;
+  c.n = min(F, n);
+  c.each = F / c.n;
+  c.more = F - c.each * c.n;
   return c;
 }
 
-// Sum of x over the CTA's PD_THREADS threads, and the sum over the threads before this one.
-__device__ __forceinline__ long long pd_scan(long long x, long long* part, long long& total) {
+__device__ __forceinline__ int pd_start(const PdCut& c, int i) { return i * c.each + min(i, c.more); }
+
+// The range that holds tile f.
+__device__ __forceinline__ int pd_range_of(const PdCut& c, int f) {
+  const int t = c.more * (c.each + 1);
+  return f < t ? f / (c.each + 1) : c.more + (f - t) / c.each;
+}
+
+// The sum of x over the CTA's PD_THREADS threads before this one, and of all.
+__device__ __forceinline__ int pd_scan(int x, int* part, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long s = x;
+  int s = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, s, d);
+    const int y = __shfl_up_sync(0xffffffffu, s, d);
     if (lane >= d) s += y;
   }
   if (lane == 31) part[warp] = s;
   __syncthreads();
-  long long before = 0;
+  int before = 0;
   total = 0;
 #pragma unroll
   for (int w = 0; w < PD_WARPS; ++w) {
-    if (w < warp) before += part[w];
-    total += part[w];
+    const int y = part[w];
+    before += w < warp ? y : 0;
+    total += y;
   }
   __syncthreads();
   return before + s - x;
 }
 
-// Tiles of all sequences (of one group of each).
-__device__ __forceinline__ long long pd_total(const PdParams& p, long long* part) {
-  if (p.prefix) return p.shared_tiles;
-  long long x = 0, total;
-  for (int b = threadIdx.x; b < p.B; b += PD_THREADS) x += pd_seq(p, b).tiles;
-  pd_scan(x, part, total);
-  return total;
+// The tiles of all sequences (of one group of each) in order.  Every thread
+// holds one of the first PD_THREADS sequences; beyond them, the sums are made
+// again when a tile is located.
+struct PdSum {
+  int total;
+  int before, tiles;    // of sequence threadIdx.x
+};
+
+// Also keeps the first PD_LENS lengths in shared memory when `lens_s` is given.
+__device__ __forceinline__ PdSum pd_sum(const PdParams& p, int* part, int* lens_s) {
+  PdSum s;
+  s.total = p.shared_tiles;
+  s.before = 0;
+  s.tiles = 0;
+  int rest = 0;
+  for (int b = threadIdx.x; b < p.B; b += PD_THREADS) {
+    const int len = pd_len_of(p, b);
+    if (lens_s != nullptr && b < PD_LENS) lens_s[b] = len;
+    const int tiles = pd_seq(p, len).tiles;
+    if (b < PD_THREADS) s.tiles = tiles;
+    else rest += tiles;
+  }
+  if (p.prefix) {
+    __syncthreads();
+    return s;
+  }
+  s.before = pd_scan(s.tiles, part, s.total);
+  if (p.B > PD_THREADS) {
+    int more;
+    pd_scan(rest, part, more);
+    s.total += more;
+  }
+  return s;
 }
 
 // The sequence that holds tile u of the sum of the sequences' tiles, and the
-// tiles before it.  `slot` holds two values of shared memory.
-__device__ __forceinline__ void pd_locate(const PdParams& p, long long u, long long* part,
-                                          long long* slot, int& b_out, long long& before_out) {
-  if (p.prefix) {
-    b_out = 0;
-    before_out = 0;
-    return;
-  }
-  long long carry = 0;
-  for (int b0 = 0; b0 < p.B; b0 += PD_THREADS) {
-    const int b = b0 + threadIdx.x;
-    const int tiles = b < p.B ? pd_seq(p, b).tiles : 0;
-    long long total;
-    const long long before = carry + pd_scan(tiles, part, total);
+// tiles before it.  part[PD_WARPS] and [PD_WARPS + 1] pass them on.
+__device__ __forceinline__ void pd_locate(const PdParams& p, const PdSum& sum, int u, int* part, int& b_out,
+                                          int& before_out) {
+  b_out = 0;
+  before_out = 0;
+  if (p.prefix) return;
+  int before = sum.before, tiles = sum.tiles, carry = 0;
+  for (int b0 = 0;;) {
     if (before <= u && u < before + tiles) {
-      slot[0] = b;
-      slot[1] = before;
+      part[PD_WARPS] = b0 + threadIdx.x;
+      part[PD_WARPS + 1] = before;
     }
-    carry += total;
+    b0 += PD_THREADS;
+    if (b0 >= p.B) break;
+    // the sum up to this chunk is the last thread's
+    if (threadIdx.x == PD_THREADS - 1) part[0] = before + tiles;
+    __syncthreads();
+    carry = part[0];
+    __syncthreads();
     if (u < carry) break;
+    const int b = b0 + threadIdx.x;
+    tiles = b < p.B ? pd_seq(p, pd_len_of(p, b)).tiles : 0;
+    int total;
+    before = carry + pd_scan(tiles, part, total);
   }
   __syncthreads();
-  b_out = static_cast<int>(slot[0]);
-  before_out = slot[1];
-  __syncthreads();
+  b_out = part[PD_WARPS];
+  before_out = part[PD_WARPS + 1];
 }
 
-// A CTA's place in its range: the current run (tiles [i, i_end) of group (b,
+// A CTA's place in its range: the current run (tiles [i0, i_end) of group (b,
 // h, rt)), and where the range goes on behind it.
 struct PdWalk {
-  long long x, end;    // flattened start of the run; end of the range
-  long long base;      // flattened start of sequence b
+  int x, end;          // flattened start of the run; end of the range
+  int base;            // flattened start of sequence b
   int b, h, rt;
   PdSeq s;
   int i0, i_end;
 };
 
 __device__ __forceinline__ void pd_run_here(const PdParams& p, PdWalk& w) {
-  const long long in = w.x - w.base;
-  const int g = static_cast<int>(in / w.s.tiles);
-  w.i0 = static_cast<int>(in - static_cast<long long>(g) * w.s.tiles);
+  const int in = w.x - w.base;
+  const int g = in / w.s.tiles;
+  w.i0 = in - g * w.s.tiles;
   w.h = g / p.row_tiles;
   w.rt = g - w.h * p.row_tiles;
-  const long long left = w.end - w.x;
-  w.i_end = static_cast<int>(left < w.s.tiles - w.i0 ? w.i0 + left : w.s.tiles);
+  w.i_end = min(w.i0 + w.end - w.x, w.s.tiles);
 }
 
-// The next run of the range, if there is one.
-__device__ __forceinline__ bool pd_next_run(const PdParams& p, PdWalk& w) {
+// The next run of the range, if there is one; it begins a group.
+__device__ __forceinline__ bool pd_next_run(const PdParams& p, PdWalk& w, const int* lens_s) {
   w.x += w.i_end - w.i0;
   if (w.x >= w.end) return false;
-  const long long all = static_cast<long long>(w.s.tiles) * p.H_kv * p.row_tiles;
-  if (w.x >= w.base + all) {
-    w.base += all;
-    w.s = pd_seq(p, ++w.b);
+  w.i0 = 0;
+  if (++w.rt == p.row_tiles) {
+    w.rt = 0;
+    if (++w.h == p.H_kv) {
+      w.h = 0;
+      w.base = w.x;
+      ++w.b;
+      w.s = pd_seq(p, w.b < PD_LENS ? lens_s[w.b] : pd_len_of(p, w.b));
+    }
   }
-  pd_run_here(p, w);
+  w.i_end = min(w.end - w.x, w.s.tiles);
   return true;
 }
 
-// First position of warp `warp`'s slice of tile i, and whether any row of the
-// sequence may keep a position of the slice (others are neither loaded nor
-// looked up in the table).
-__device__ __forceinline__ bool pd_slice(const PdParams& p, const PdSeq& s, int i, int warp, int& key0) {
-  key0 = (i < s.sb ? i : s.w0 + (i - s.sb)) * PD_TILE + warp * PD_SLICE;
-  if (key0 >= s.len) return false;
-  if (p.window > 0 && key0 >= p.n_sink && key0 + PD_SLICE - 1 < s.len - p.N_q - p.window + 1) return false;
-  return true;
+// First position of warp `warp`'s slice of tile i.
+__device__ __forceinline__ int pd_key(const PdSeq& s, int i, int warp) {
+  return (i < s.sb ? i : s.w0 + (i - s.sb)) * PD_TILE + warp * PD_SLICE;
+}
+
+// The run's tiles [i0, pd_stop) hold positions of the warp's slice.
+__device__ __forceinline__ int pd_stop(const PdWalk& w, int warp) {
+  const int t = max(0, w.s.len - warp * PD_SLICE + PD_TILE - 1) / PD_TILE;
+  return min(w.i_end, t > w.s.w0 ? w.s.sb + t - w.s.w0 : min(w.s.sb, t));
+}
+
+// Under a window, whether no row of the sequence keeps a position of the slice
+// at key0: it is neither loaded nor looked up in the table.
+__device__ __forceinline__ bool pd_gone(const PdParams& p, const PdSeq& s, int key0) {
+  return p.window > 0 && key0 >= p.n_sink && key0 + PD_SLICE - 1 < s.len - p.N_q - p.window + 1;
 }
 
 // ------------------------------------------------------------ warp pieces
@@ -232,6 +298,17 @@ __device__ __forceinline__ void pd_ldsm(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void pd_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* a) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values, two of a row a lane.
+__device__ __forceinline__ uint32_t pd_transpose(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // c += a b, 16 x 8 x 16, fp32 accumulation.
@@ -247,63 +324,66 @@ __device__ __forceinline__ void pd_mma(float (&c)[4], const uint32_t (&a)[4], ui
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A query row of a group: its index in q, o and lse, and the positions it
-// keeps: j <= hi, and j >= lo or j < n_sink.
-struct PdRow {
-  bool real;
-  size_t idx;
-  int hi, lo;
-};
+// The rows of a run's group: row r of the tile is row r_first + r of the R
+// rows of sequence w.b and K/V head w.h, or, in the prefix, of the B * R rows
+// of that head.
+__device__ __forceinline__ int pd_rows(const PdParams& p, const PdWalk& w) {
+  return min(p.m, (p.prefix ? p.B * p.R : p.R) - w.rt * p.m);
+}
 
-__device__ __forceinline__ PdRow pd_row(const PdParams& p, const PdWalk& w, int r_in_tile) {
-  PdRow x;
-  int b = w.b, r = w.rt * PD_M + r_in_tile;
+// Index of row r in q, o and lse (r < pd_rows).
+__device__ __forceinline__ size_t pd_row_index(const PdParams& p, const PdWalk& w, int r) {
+  int b = w.b;
+  r += w.rt * p.m;
   if (p.prefix) {
     b = r / p.R;
     r -= b * p.R;
-    x.real = b < p.B;
-  } else {
-    x.real = r < p.R;
   }
-  x.idx = 0;
-  x.hi = -1;
-  x.lo = 0;
-  if (!x.real) return x;
-  const int head = r / p.N_q, i = r - head * p.N_q;
-  x.idx = (static_cast<size_t>(b) * p.H + w.h * p.G + head) * p.N_q + i;
+  return (static_cast<size_t>(b) * p.H + w.h * p.G) * p.N_q + r;
+}
+
+// The positions that row r (r < pd_rows) keeps: j <= hi, and j >= lo or j < n_sink.
+__device__ __forceinline__ void pd_row_keeps(const PdParams& p, const PdWalk& w, int r, const int* lens_s,
+                                             int& hi, int& lo) {
   int len = w.s.len;
-  if (p.prefix) len = min(max(p.lens[b], 0), p.max_pages << p.page_shift);
-  const int pos = len - p.N_q + i;
-  x.hi = p.causal ? pos : len - 1;
-  if (p.prefix) x.hi = min(x.hi, w.s.len - 1);
-  if (p.window > 0) x.lo = pos - p.window + 1;
-  return x;
+  r += w.rt * p.m;
+  if (p.prefix) {
+    const int b = r / p.R;
+    r -= b * p.R;
+    len = b < PD_LENS ? lens_s[b] : pd_len_of(p, b);
+  }
+  const int pos = len - p.N_q + (p.N_q == 1 ? 0 : r % p.N_q);
+  hi = p.causal ? pos : len - 1;
+  if (p.prefix) hi = min(hi, w.s.len - 1);
+  lo = p.window > 0 ? pos - p.window + 1 : 0;
 }
 
 // ------------------------------------------------------------ attending kernel
 
 // Each warp streams its own slices: slice `warp` of every tile of the range,
 // through its own ring of TMA loads, with its own running (m, l, O) for the
-// group's PD_M rows in registers (mma.sync 16 x 8 x 16; rows past R are
-// padding).  No warp waits for another before the end of a run, where the
-// eight results are combined through shared memory.  The next runs' slices are
-// in flight meanwhile.
+// group's rows in registers.  No warp waits for another before the end of a
+// run, where the warps' results are combined through shared memory; the next
+// runs' slices are in flight meanwhile.
 //
-// Bound: HBM.  A slice is 16 rows of K and of V; 8 warps x PD_NST slices keep
-// 192 KB a SM in flight.  The tensor work of 16 padded rows is small against
-// that (rows are few: a group's query heads times new rows), so the
-// instruction with the smallest M is taken; tcgen05's 128 rows would do
-// eight times the work and exponentials.
-template <int D, bool BF16, bool OUT_F32>
-__global__ void __launch_bounds__(PD_THREADS, 1)
+// Bound: HBM.  A slice is 16 rows of K and of V; two CTAs' rings keep 192 KB
+// a SM in flight.  With two warps on each scheduler the instructions of a
+// slice bound the rate next, so they are kept few.  The products are taken
+// transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync 16 x 8 x 16, 16
+// positions or 16 columns by 8 query rows), so that up to 8 rows, the query heads
+// of a K/V head at one new row each, cost half of what a 16-row tile of Q would;
+// tcgen05's 128 rows would cost 16 times that and as many more exponentials.
+template <int D, int NT, bool BF16, bool OUT_F32>
+__global__ void __launch_bounds__(PD_THREADS, 2)
 attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const PdParams p) {
-  using T = PdGeo<D>;
+  using T = PdGeo<D, NT>;
+  constexpr int M = T::M;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  long long* part = reinterpret_cast<long long*>(smem + T::SCAN_OFF);
-  long long* slot = part + PD_WARPS;
+  int* part = reinterpret_cast<int*>(smem + T::SCAN_OFF);
+  int* lens_s = reinterpret_cast<int*>(smem + T::LENS_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::ABORT_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t ring = smem_addr(smem) + warp * T::NST * T::STAGE_BYTES;
@@ -323,6 +403,104 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   grid_launch_dependents();
   __syncthreads();
 
+  const int HR = p.H_kv * p.row_tiles;
+  const PdSum sum = pd_sum(p, part, lens_s);
+  const PdCut cut = pd_cut(sum.total * HR, gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= cut.n) return;
+  PdWalk w;
+  const int f0 = pd_start(cut, blockIdx.x);
+  w.x = f0;
+  w.end = pd_start(cut, blockIdx.x + 1);
+  pd_locate(p, sum, w.x / HR, part, w.b, w.base);
+  w.base *= HR;
+  w.s = pd_seq(p, w.b < PD_LENS ? lens_s[w.b] : pd_len_of(p, w.b));
+  pd_run_here(p, w);
+
+  // ---- this warp's loads: the slice to load next.  Lane l looks up the page of
+  // this warp's slice of tile l_base + l, 32 tiles at a time.
+  PdWalk lw = w;
+  int li = lw.i0 - 1, l_stop = pd_stop(lw, warp), l_base = -32, l_pages = 0;
+  bool l_more = true;
+  uint32_t l_stage = 0;
+  uint32_t loaded = 0;
+  auto advance = [&]() {
+    for (;;) {
+      if (++li >= l_stop) {
+        l_more = pd_next_run(p, lw, lens_s);
+        if (!l_more) return;
+        l_stop = pd_stop(lw, warp);
+        li = -1;
+        l_base = -32;
+        if (warp == 0 && lane < pd_rows(p, lw))
+          prefetch_l2(static_cast<const uint16_t*>(p.q) + pd_row_index(p, lw, lane) * D);
+        continue;
+      }
+      if (li >= l_base + 32 || l_base < 0) {
+        l_base = li;
+        l_pages = -1;
+        const int key = pd_key(lw.s, li + lane, warp);
+        if (li + lane < l_stop && !pd_gone(p, lw.s, key))
+          l_pages = p.table[(p.prefix ? 0 : static_cast<size_t>(lw.b) * p.max_pages) + (key >> p.page_shift)];
+      }
+      if (!pd_gone(p, lw.s, pd_key(lw.s, li, warp))) break;
+    }
+  };
+  auto refill = [&]() {
+    if (!l_more) return;
+    const int l_page = __shfl_sync(0xffffffffu, l_pages, li - l_base);
+    if (elect_one()) {
+      const uint32_t bar = bars + 8 * l_stage;
+      const uint32_t dst = ring + l_stage * T::STAGE_BYTES;
+      const bool good = static_cast<unsigned>(l_page) < static_cast<unsigned>(p.n_pages);
+      // a bad page's box lies outside the tensor and is filled with zeros
+      const int z = good ? l_page * p.H_kv + lw.h : -1;
+      const int y = pd_key(lw.s, li, warp) & ((1 << p.page_shift) - 1);
+      if (!good) atomicCAS(p.status, 0, -1);
+      if (!p.withhold_loads) {
+        mbar_arrive_expect_tx(bar, T::STAGE_BYTES);
+        tma_load_4d(dst, &tmK, bar, 0, y, 0, z);
+        tma_load_4d(dst + T::HALF_BYTES, &tmV, bar, 0, y, 0, z);
+      }
+    }
+    __syncwarp();
+    ++loaded;
+    if (++l_stage == T::NST) l_stage = 0;
+    advance();
+  };
+
+  // ---- a run's rows.  They go through shared memory (fetch, store), from
+  // where every warp takes the B operands.
+  const uint32_t q_tile = smem_addr(smem) + T::Q_OFF;
+  struct QPart {
+    uint4 x[(T::Q_VECS + PD_THREADS - 1) / PD_THREADS];
+  };
+  auto fetch_q = [&]() {
+    QPart f;
+    const int n = pd_rows(p, w);
+#pragma unroll
+    for (int u = 0; u * PD_THREADS < T::Q_VECS; ++u) {
+      const int r = (threadIdx.x + u * PD_THREADS) / (D / 8), c = (threadIdx.x + u * PD_THREADS) % (D / 8);
+      f.x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < n)
+        f.x[u] = *(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + pd_row_index(p, w, r) * D) + c);
+    }
+    return f;
+  };
+  auto store_q = [&](const QPart& f) {
+#pragma unroll
+    for (int u = 0; u * PD_THREADS < T::Q_VECS; ++u) {
+      const int r = (threadIdx.x + u * PD_THREADS) / (D / 8), c = (threadIdx.x + u * PD_THREADS) % (D / 8);
+      if (r < M)
+        st_shared_v4(q_tile + (c >> 3) * T::Q_CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4), f.x[u].x, f.x[u].y,
+                     f.x[u].z, f.x[u].w);
+    }
+  };
+  {
+    const QPart x = fetch_q();
+    advance();
+    for (int s = 0; s < T::NST; ++s) refill();
+    store_q(x);
+  }
   // lengths that do not fit the table are reported once
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < p.B; b += PD_THREADS) {
@@ -330,320 +508,304 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (n < 0 || n > (p.max_pages << p.page_shift)) atomicCAS(p.status, 0, -1);
     }
   }
-  const int HR = p.H_kv * p.row_tiles;
-  const long long F = pd_total(p, part) * HR;
-  const int ranges = static_cast<int>(F < gridDim.x ? F : gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= ranges) return;
-  PdWalk w;
-  const long long f0 = pd_start(blockIdx.x, F, ranges);
-  w.x = f0;
-  w.end = pd_start(blockIdx.x + 1, F, ranges);
-  {
-    long long before;
-    pd_locate(p, w.x / HR, part, slot, w.b, before);
-    w.base = before * HR;
-  }
-  w.s = pd_seq(p, w.b);
-  pd_run_here(p, w);
+  __syncthreads();
 
-  // ---- this warp's loads: the slice to load next, and its page
-  PdWalk lw = w;
-  int li = lw.i0 - 1, l_key0 = 0, l_page = 0;
-  bool l_more = true;
-  uint32_t loaded = 0;
-  auto advance = [&]() {
-    for (;;) {
-      if (++li >= lw.i_end) {
-        l_more = pd_next_run(p, lw);
-        if (!l_more) return;
-        li = lw.i0;
-      }
-      if (pd_slice(p, lw.s, li, warp, l_key0)) break;
-    }
-    const int col = l_key0 >> p.page_shift;
-    l_page = p.table[(p.prefix ? 0 : static_cast<size_t>(lw.b) * p.max_pages) + col];
-  };
-  auto refill = [&]() {
-    if (!l_more) return;
-    const int st = loaded % T::NST;
-    const uint32_t bar = bars + 8 * st;
-    const uint32_t dst = ring + st * T::STAGE_BYTES;
-    const bool good = static_cast<unsigned>(l_page) < static_cast<unsigned>(p.n_pages);
-    // a bad page's box lies outside the tensor and is filled with zeros
-    const int z = good ? l_page * p.H_kv + lw.h : -1;
-    const int y = l_key0 & ((1 << p.page_shift) - 1);
-    if (elect_one()) {
-      if (!good) atomicCAS(p.status, 0, -1);
-      if (!p.withhold_loads) {
-        mbar_arrive_expect_tx(bar, T::STAGE_BYTES);
-#pragma unroll
-        for (int c = 0; c < T::NCH; ++c)
-          tma_load_3d(dst + c * T::CHUNK_BYTES, &tmK, bar, c * 64, y, z);
-#pragma unroll
-        for (int c = 0; c < T::NCH; ++c)
-          tma_load_3d(dst + T::HALF_BYTES + c * T::CHUNK_BYTES, &tmV, bar, c * 64, y, z);
-      }
-    }
-    __syncwarp();
-    ++loaded;
-    advance();
-  };
-  advance();
-  for (int s = 0; s < T::NST; ++s) refill();
-
+  // Fragments: lane 4 g + t holds positions g and g + 8 (of K's slice) or
+  // columns g and g + 8 (of V's 16), and query rows 8 n + 2 t and 8 n + 2 t + 1.
   const int g = lane >> 2, t = lane & 3;
   // A scale of 0 (every kept logit 0) is run as 1e-30: the logits then stay
-  // within 1e-25 of 0, every weight rounds to exactly 1 in fp32 as for 0.
-  const float c = p.scale_log2 != 0.f ? p.scale_log2 : 1e-30f;
-  // ldmatrix row addresses: lane -> row (lane & 7) of 8 x 8 matrix lane / 8.
-  // K: matrices (rows 0-7, d 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15);
-  // V, transposed: (0-7, 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15).
+  // within 1e-25 of 0, every weight rounds to exactly 1 in fp32 as for 0.  A
+  // negative scale turns the signs of Q.
+  const float c = p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1e-30f;
+  const uint32_t q_sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+  // ldmatrix: lane -> row lane & 7 of 8 x 8 matrix lane / 8.  K: matrices
+  // (positions 0-7, d 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15); V,
+  // transposed: (0-7, 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15).  The four
+  // column pairs of a 128-byte row, swizzled, are four offsets.
   const int mat = lane >> 3, mr = lane & 7;
-  const uint32_t k_row = static_cast<uint32_t>((mat >> 1) * 8 + mr) * 128;
-  const uint32_t v_row = static_cast<uint32_t>((mat & 1) * 8 + mr) * 128;
-  const int k_col = mat & 1, v_col = mat >> 1;
+  uint32_t k_off[4], v_off[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    k_off[k] = ((mat & 1) * 8 + mr) * 128 + (((2 * k + (mat >> 1)) ^ mr) << 4);
+    v_off[k] = ((mat >> 1) * 8 + mr) * 128 + (((2 * k + (mat & 1)) ^ mr) << 4);
+  }
+  constexpr uint32_t one2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
+  const uint32_t ones[4] = {one2, one2, one2, one2};
   uint32_t done = 0, waited = 0;   // slices passed; slices whose loads have landed
+  uint32_t stage = 0, phase = 0;
   bool ok = true;
 
   for (bool more = true; more;) {
-    // ---- the run's rows
-    const PdRow row0 = pd_row(p, w, g), row1 = pd_row(p, w, g + 8);
-    uint32_t qf[D / 16][4];
-    {
-      const uint32_t* q0 = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + row0.idx * D) + t;
-      const uint32_t* q1 = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + row1.idx * D) + t;
+    uint32_t qf[D / 16][NT][2];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][0] = row0.real ? q0[8 * k] : 0u;
-        qf[k][1] = row1.real ? q1[8 * k] : 0u;
-        qf[k][2] = row0.real ? q0[8 * k + 4] : 0u;
-        qf[k][3] = row1.real ? q1[8 * k + 4] : 0u;
+    for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t x[4];
+        pd_ldsm(q_tile + (k >> 1) * T::Q_CHUNK + (n * 8 + mr) * 128 + ((((k & 1) * 4 + mat) ^ mr) << 4), x);
+        qf[2 * k][n][0] = x[0] ^ q_sign;
+        qf[2 * k][n][1] = x[1] ^ q_sign;
+        qf[2 * k + 1][n][0] = x[2] ^ q_sign;
+        qf[2 * k + 1][n][1] = x[3] ^ q_sign;
       }
+    // limits of this lane's rows, and the positions that some row keeps and
+    // that all rows keep
+    int hi[NT][2], lo[NT][2];
+    int hi_max = -1, hi_min = INT_MAX, lo_min = INT_MAX, lo_max = INT_MIN;
+    {
+      const int n_rows = pd_rows(p, w);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * t + e;
+          hi[n][e] = -1;
+          lo[n][e] = 0;
+          if (r < n_rows) {
+            pd_row_keeps(p, w, r, lens_s, hi[n][e], lo[n][e]);
+            hi_max = max(hi_max, hi[n][e]);
+            hi_min = min(hi_min, hi[n][e]);
+            lo_min = min(lo_min, lo[n][e]);
+            lo_max = max(lo_max, lo[n][e]);
+          }
+        }
+      hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+      hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+      lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+      lo_max = __reduce_max_sync(0xffffffffu, lo_max);
     }
-    // positions that some row keeps, and that all rows keep
-    int hi_max = max(row0.hi, row1.hi);
-    int hi_min = min(row0.real ? row0.hi : INT_MAX, row1.real ? row1.hi : INT_MAX);
-    int lo_min = min(row0.real ? row0.lo : INT_MAX, row1.real ? row1.lo : INT_MAX);
-    int lo_max = max(row0.real ? row0.lo : INT_MIN, row1.real ? row1.lo : INT_MIN);
-    hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-    hi_min = __reduce_min_sync(0xffffffffu, hi_min);
-    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
-    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
 
-    float acc[D / 8][4];
+    float acc[D / 16][NT][4];
+    float lsum[NT][4];          // sums of the rounded weights, by the tensor cores
+    float m[NT][2], le[NT][2];  // maximum (log2 units), sum of the exact weights
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY;
-    float le0 = 0.f, le1 = 0.f, lr0 = 0.f, lr1 = 0.f;   // sums of exact and of rounded weights
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[k][n][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) lsum[n][e] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      le[n][0] = le[n][1] = 0.f;
+    }
 
-    for (int i = w.i0; i < w.i_end; ++i) {
-      int key0;
-      if (!pd_slice(p, w.s, i, warp, key0)) continue;
-      const int st = done % T::NST;
+    const int i_stop = pd_stop(w, warp);
+    for (int i = w.i0; i < i_stop; ++i) {
+      const int key0 = pd_key(w.s, i, warp);
+      if (pd_gone(p, w.s, key0)) continue;
+      const uint32_t ks = ring + stage * T::STAGE_BYTES, vs = ks + T::HALF_BYTES;
       if (ok) {
-        const uint32_t par = (done / T::NST) & 1u;
-        ok = mbar_try_wait(bars + 8 * st, par) ||
-             wait_slow(bars + 8 * st, par, abort_flag, p.status, p.watchdog_ns);
+        const uint32_t bar = bars + 8 * stage;
+        ok = mbar_try_wait(bar, phase) || wait_slow(bar, phase, abort_flag, p.status, p.watchdog_ns);
         ok = __all_sync(0xffffffffu, ok);
       }
       ++done;
+      if (++stage == T::NST) {
+        stage = 0;
+        phase ^= 1u;
+      }
       if (!ok) continue;
       waited = done;
-      const uint32_t ks = ring + st * T::STAGE_BYTES, vs = ks + T::HALF_BYTES;
-      float s[2][4] = {};
+      // S^T, the even and the odd steps of d summed apart (two chains)
+      float s[NT][4] = {}, s2[NT][4] = {};
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t kf[4];
-        const int u = (k & 3) * 2 + k_col;   // 16-byte unit of the 128-byte chunk row
-        pd_ldsm(ks + (k >> 2) * T::CHUNK_BYTES + k_row + ((u ^ mr) << 4), kf);
-        pd_mma<BF16>(s[0], qf[k], kf[0], kf[1]);
-        pd_mma<BF16>(s[1], qf[k], kf[2], kf[3]);
+        pd_ldsm(ks + (k >> 2) * T::CHUNK_BYTES + k_off[k & 3], kf);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) pd_mma<BF16>((k & 1) ? s2[n] : s[n], kf, qf[k][n][0], qf[k][n][1]);
       }
-      // log2 units
+      bool up = false;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] *= c;
+        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
       const bool masked = key0 + PD_SLICE - 1 > hi_min ||
                           (p.window > 0 && key0 < lo_max && key0 + PD_SLICE > p.n_sink);
       if (masked) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = key0 + n * 8 + 2 * t + e;
-            const bool sink = p.window == 0 || j < p.n_sink;
-            if (!(j <= row0.hi && (sink || j >= row0.lo))) s[n][e] = -INFINITY;
-            if (!(j <= row1.hi && (sink || j >= row1.lo))) s[n][2 + e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            const int j = key0 + g + (e >> 1) * 8;
+            const bool keep = j <= hi[n][e & 1] && (p.window == 0 || j >= lo[n][e & 1] || j < p.n_sink);
+            if (!keep) s[n][e] = -INFINITY;
           }
       }
-      float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-      // lazy rescale: the stale maximum is kept until a row's grows by 2^8
-      const bool up0 = x0 > m0 + RESCALE_THRESHOLD, up1 = x1 > m1 + RESCALE_THRESHOLD;
-      if (__any_sync(0xffffffffu, up0 || up1)) {
-        const float a0 = up0 ? (m0 == -INFINITY ? 0.f : fast_exp2(m0 - x0)) : 1.f;
-        const float a1 = up1 ? (m1 == -INFINITY ? 0.f : fast_exp2(m1 - x1)) : 1.f;
-        if (up0) m0 = x0;
-        if (up1) m1 = x1;
-        le0 *= a0; lr0 *= a0; le1 *= a1; lr1 *= a1;
+      // lazy rescale: the stale maximum is kept until a row's grows by 2^8;
+      // only then do the lanes that share a row agree on it
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          acc[n][0] *= a0; acc[n][1] *= a0;
-          acc[n][2] *= a1; acc[n][3] *= a1;
-        }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) up |= fmaxf(s[n][e], s[n][e + 2]) * c > m[n][e] + RESCALE_THRESHOLD;
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[n][e], s[n][e + 2]) * c;
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const bool grow = x > m[n][e] + RESCALE_THRESHOLD;
+            const float a = grow ? (m[n][e] == -INFINITY ? 0.f : fast_exp2(m[n][e] - x)) : 1.f;
+            if (grow) m[n][e] = x;
+            le[n][e] *= a;
+            lsum[n][e] *= a;
+            lsum[n][e + 2] *= a;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              acc[k][n][e] *= a;
+              acc[k][n][e + 2] *= a;
+            }
+          }
       }
-      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-      uint32_t pf[4];
+      uint32_t pf[NT][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float p0 = fast_exp2(s[n][0] - r0), p1 = fast_exp2(s[n][1] - r0);
-        const float p2 = fast_exp2(s[n][2] - r1), p3 = fast_exp2(s[n][3] - r1);
-        pf[2 * n] = pack2<BF16>(p0, p1);
-        pf[2 * n + 1] = pack2<BF16>(p2, p3);
-        le0 += p0 + p1;
-        le1 += p2 + p3;
+      for (int n = 0; n < NT; ++n) {
+        const float r0 = m[n][0] == -INFINITY ? 0.f : -m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : -m[n][1];
+        const float p0 = fast_exp2(fmaf(s[n][0], c, r0)), p1 = fast_exp2(fmaf(s[n][1], c, r1));
+        const float p2 = fast_exp2(fmaf(s[n][2], c, r0)), p3 = fast_exp2(fmaf(s[n][3], c, r1));
+        le[n][0] += p0 + p2;
+        le[n][1] += p1 + p3;
+        pf[n][0] = pd_transpose(pack2<BF16>(p0, p1));
+        pf[n][1] = pd_transpose(pack2<BF16>(p2, p3));
         // O is divided by the sum of the weights as they are multiplied (16
         // bits), so that their rounding errors partly cancel
-        lr0 += unpack_lo<BF16>(pf[2 * n]) + unpack_hi<BF16>(pf[2 * n]);
-        lr1 += unpack_lo<BF16>(pf[2 * n + 1]) + unpack_hi<BF16>(pf[2 * n + 1]);
+        pd_mma<BF16>(lsum[n], ones, pf[n][0], pf[n][1]);
       }
       // V rows that no row of the group keeps count as zeros: their weight is
       // 0, and 0 times what such a row holds could be NaN
-      uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
       const bool holes = masked && (key0 + PD_SLICE - 1 > hi_max ||
                                     (p.window > 0 && key0 < lo_min && key0 + PD_SLICE > p.n_sink));
-      if (holes) {
+      if (!holes) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t vf[4];
+          pd_ldsm_t(vs + (k >> 2) * T::CHUNK_BYTES + v_off[k & 3], vf);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) pd_mma<BF16>(acc[k][n], vf, pf[n][0], pf[n][1]);
+        }
+      } else {
         auto bits = [&](int j) {
           const bool k0 = j <= hi_max && (p.window == 0 || j >= lo_min || j < p.n_sink);
           const bool k1 = j + 1 <= hi_max && (p.window == 0 || j + 1 >= lo_min || j + 1 < p.n_sink);
           return (k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u);
         };
-        keep_lo = bits(key0 + 2 * t);
-        keep_hi = bits(key0 + 8 + 2 * t);
-      }
+        const uint32_t first = bits(key0 + 2 * t), second = bits(key0 + 8 + 2 * t);
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
-        uint32_t vf[4];
-        const int u = (n & 3) * 2 + v_col;
-        pd_ldsm_t(vs + (n >> 2) * T::CHUNK_BYTES + v_row + ((u ^ mr) << 4), vf);
-        if (holes) {
-          vf[0] &= keep_lo;
-          vf[1] &= keep_hi;
-          vf[2] &= keep_lo;
-          vf[3] &= keep_hi;
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t vf[4];
+          pd_ldsm_t(vs + (k >> 2) * T::CHUNK_BYTES + v_off[k & 3], vf);
+          vf[0] &= first;
+          vf[1] &= first;
+          vf[2] &= second;
+          vf[3] &= second;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) pd_mma<BF16>(acc[k][n], vf, pf[n][0], pf[n][1]);
         }
-        pd_mma<BF16>(acc[2 * n], pf, vf[0], vf[1]);
-        pd_mma<BF16>(acc[2 * n + 1], pf, vf[2], vf[3]);
       }
       __syncwarp();   // every lane has read the stage
       refill();
     }
 
-    // ---- the run's result: the eight warps' (m, l, O) combined
-    le0 += __shfl_xor_sync(0xffffffffu, le0, 1);
-    le1 += __shfl_xor_sync(0xffffffffu, le1, 1);
-    lr0 += __shfl_xor_sync(0xffffffffu, lr0, 1);
-    lr1 += __shfl_xor_sync(0xffffffffu, lr1, 1);
-    le0 += __shfl_xor_sync(0xffffffffu, le0, 2);
-    le1 += __shfl_xor_sync(0xffffffffu, le1, 2);
-    lr0 += __shfl_xor_sync(0xffffffffu, lr0, 2);
-    lr1 += __shfl_xor_sync(0xffffffffu, lr1, 2);
-    if (t == 0) {
-      float* sw = stat + warp * PD_M;
-      sw[g] = m0;
-      sw[g + 8] = m1;
-      sw[PD_WARPS * PD_M + g] = le0;
-      sw[PD_WARPS * PD_M + g + 8] = le1;
-      sw[2 * PD_WARPS * PD_M + g] = lr0;
-      sw[2 * PD_WARPS * PD_M + g + 8] = lr1;
-    }
-    // this thread's share of the result: 4 columns of every 64 of one row
-    const int orow = threadIdx.x >> 4, oc = threadIdx.x & 15;
-    const PdRow out = pd_row(p, w, orow);
-    const long long g_start = w.x - w.i0;
-    const int c_first = pd_range_of(g_start, F, ranges);
-    const int c_last = pd_range_of(g_start + w.s.tiles - 1, F, ranges);
-    const bool split = c_first != c_last;
+    // ---- the run's result: the warps' (m, l, O) combined
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = le[n][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) {
+          float* sw = stat + warp * M + 8 * n + 2 * t + e;
+          sw[0] = m[n][e];
+          sw[PD_WARPS * M] = x;
+          sw[2 * PD_WARPS * M] = lsum[n][e];
+        }
+      }
+    // where the result goes: the output, or for a split group the slot of the
+    // range's first (0) or of another run (1), or else the group's own place
+    const int g_start = w.x - w.i0;
+    const bool split = pd_range_of(cut, g_start) != pd_range_of(cut, g_start + w.s.tiles - 1);
     const bool direct = !split && !p.prefix && p.shared_tiles == 0;
-    const long long group = static_cast<long long>(w.b) * HR + w.h * p.row_tiles + w.rt;
-    // a split group's run: the range's first one in slot 0, another in slot 1
-    float* po;
-    float* pl;
-    if (split) {
-      const size_t sl = 2 * static_cast<size_t>(blockIdx.x) + (w.x == f0 ? 0 : 1);
-      po = p.part_o + (sl * PD_M + orow) * D;
-      pl = p.part_lse + sl * PD_M + orow;
-    } else {
-      po = p.own_o + (static_cast<size_t>(group) * PD_M + orow) * D;
-      pl = p.own_lse + static_cast<size_t>(group) * PD_M + orow;
-    }
-    float wt[PD_WARPS], M = 0.f, le = 0.f, inv = 0.f;
+    const int n_rows = pd_rows(p, w);
+    size_t row;
+    float* po = split ? p.part_o : p.own_o;
+    float* pl = split ? p.part_lse : p.own_lse;
+    if (direct)
+      row = pd_row_index(p, w, 0);
+    else if (split)
+      row = (2 * static_cast<size_t>(blockIdx.x) + (w.x == f0 ? 0 : 1)) * M;
+    else
+      row = (static_cast<size_t>(w.b) * HR + w.h * p.row_tiles + w.rt) * M;
+    // the next run's rows are on their way while this one is finished
+    more = pd_next_run(p, w, lens_s);
+    QPart q_next;
+    if (more) q_next = fetch_q();
+
+    constexpr int XR = T::X_ROWS;
 #pragma unroll
-    for (int half = 0; half < D / 64; ++half) {
-      float* xw = xbuf + warp * PD_M * 64;
+    for (int r0 = 0; r0 < M; r0 += XR) {
+      if (r0 >= n_rows) break;
+      // rows [r0, r0 + XR) of this warp's O; rows 4 apart in bank and columns
+      // side by side, so the stores of a warp hit every bank once
+      if (XR == 8 || (t >> 1) == ((r0 >> 2) & 1)) {
+        float* xw = xbuf + (warp * XR + ((2 * t) & (XR - 1))) * T::X_LD + g;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        // 8-byte units of a row are swapped by the row, so that a half-warp's
-        // stores hit every bank once
-        const int u = (n * 4 + t) ^ ((g & 3) * 4);
-        *reinterpret_cast<float2*>(xw + g * 64 + u * 2) = make_float2(acc[half * 8 + n][0], acc[half * 8 + n][1]);
-        *reinterpret_cast<float2*>(xw + (g + 8) * 64 + u * 2) = make_float2(acc[half * 8 + n][2], acc[half * 8 + n][3]);
-      }
-      __syncthreads();
-      if (half == 0) {
-        M = -INFINITY;
-#pragma unroll
-        for (int v = 0; v < PD_WARPS; ++v) M = fmaxf(M, stat[v * PD_M + orow]);
-        const float mr_ = M == -INFINITY ? 0.f : M;
-        float lr = 0.f;
-#pragma unroll
-        for (int v = 0; v < PD_WARPS; ++v) {
-          wt[v] = fast_exp2(stat[v * PD_M + orow] - mr_);
-          le += wt[v] * stat[(PD_WARPS + v) * PD_M + orow];
-          lr += wt[v] * stat[(2 * PD_WARPS + v) * PD_M + orow];
-        }
-        inv = le == 0.f ? 0.f : 1.f / lr;
-      }
-      if (out.real) {
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int v = 0; v < PD_WARPS; ++v) {
-          const float* xr = xbuf + (v * PD_M + orow) * 64;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 y = *reinterpret_cast<const float2*>(xr + (((2 * oc + e) ^ ((orow & 3) * 4)) * 2));
-            o[2 * e] = fmaf(wt[v], y.x, o[2 * e]);
-            o[2 * e + 1] = fmaf(wt[v], y.y, o[2 * e + 1]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= inv;
-        const int col = half * 64 + oc * 4;
-        if (!direct) {
-          *reinterpret_cast<float4*>(po + col) = make_float4(o[0], o[1], o[2], o[3]);
-        } else if constexpr (OUT_F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out.idx * D + col) =
-              make_float4(o[0], o[1], o[2], o[3]);
-        } else {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out.idx * D + col) =
-              make_uint2(pack2<BF16>(o[0], o[1]), pack2<BF16>(o[2], o[3]));
-        }
-        if (half == 0 && oc == 0) {
-          const float z = le == 0.f ? -INFINITY : (M + log2f(le)) * 0.69314718055994531f;
-          if (!direct) *pl = z;
-          else if (p.lse != nullptr) p.lse[out.idx] = z;
+        for (int k = 0; k < D / 16; ++k) {
+          const float (&a)[4] = acc[k][r0 / 8];
+          xw[16 * k] = a[0];
+          xw[16 * k + T::X_LD] = a[1];
+          xw[16 * k + 8] = a[2];
+          xw[16 * k + 8 + T::X_LD] = a[3];
         }
       }
       __syncthreads();
+      if (more && r0 + XR >= n_rows) store_q(q_next);   // every warp has its B operands
+      // this thread: four columns of one row
+      const int xr = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4), r = r0 + xr;
+      if (r < n_rows) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < PD_WARPS; ++v) top = fmaxf(top, stat[v * M + r]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float l_exact = 0.f, l_round = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < PD_WARPS; ++v) {
+          const float wt = fast_exp2(stat[v * M + r] - ref);
+          l_exact = fmaf(wt, stat[(PD_WARPS + v) * M + r], l_exact);
+          l_round = fmaf(wt, stat[(2 * PD_WARPS + v) * M + r], l_round);
+          const float4 y = *reinterpret_cast<const float4*>(xbuf + (v * XR + xr) * T::X_LD + c4 * 4);
+          o.x = fmaf(wt, y.x, o.x);
+          o.y = fmaf(wt, y.y, o.y);
+          o.z = fmaf(wt, y.z, o.z);
+          o.w = fmaf(wt, y.w, o.w);
+        }
+        const float inv = l_exact == 0.f ? 0.f : 1.f / l_round;
+        o.x *= inv;
+        o.y *= inv;
+        o.z *= inv;
+        o.w *= inv;
+        const size_t at = (row + r) * D + c4 * 4;
+        if (!direct)
+          *reinterpret_cast<float4*>(po + at) = o;
+        else if constexpr (OUT_F32)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = o;
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
+              make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
+        if (c4 == 0) {
+          const float z = l_exact == 0.f ? -INFINITY : (top + log2f(l_exact)) * 0.69314718055994531f;
+          if (!direct) pl[row + r] = z;
+          else if (p.lse != nullptr) p.lse[row + r] = z;
+        }
+      }
+      __syncthreads();
     }
-    more = pd_next_run(p, w);
   }
   // after an expired wait, the copies still in flight
   if (!ok && !p.withhold_loads) {
@@ -659,35 +821,35 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 struct PdParts {
   const float* o;
   const float* lse;
-  int n, c0;
-  size_t row;       // row of the first part, in rows of PD_M a slot or group
-  size_t row_next;  // row of the second part; the others follow 2 * PD_M apart
+  int n;
+  size_t row;       // row of the first part, in rows of m a slot or group
+  size_t row_next;  // row of the second part; the others follow `step` apart
+  int step;
 };
 
-// The parts of group `group`, whose tiles [start, start + tiles) lie in
-// `ranges` ranges of F tiles.
-__device__ __forceinline__ PdParts pd_parts(const PdParams& p, long long start, int tiles, long long F,
-                                            int ranges, size_t group, int row) {
+// The parts of group `group`, whose tiles are [start, start + tiles).
+__device__ __forceinline__ PdParts pd_parts(const PdParams& p, const PdCut& cut, int start, int tiles,
+                                            size_t group, int row) {
   PdParts x;
-  const int c0 = pd_range_of(start, F, ranges), c1 = pd_range_of(start + tiles - 1, F, ranges);
+  const int c0 = pd_range_of(cut, start), c1 = pd_range_of(cut, start + tiles - 1);
   x.n = c1 - c0 + 1;
-  x.c0 = c0;
   if (x.n == 1) {
     x.o = p.own_o;
     x.lse = p.own_lse;
-    x.row = group * PD_M + row;
+    x.row = group * p.m + row;
   } else {
     x.o = p.part_o;
     x.lse = p.part_lse;
     // the first part is its range's last run, the others their ranges' first
-    x.row = (2 * static_cast<size_t>(c0) + (start != pd_start(c0, F, ranges) ? 1 : 0)) * PD_M + row;
+    x.row = (2 * static_cast<size_t>(c0) + (start != pd_start(cut, c0) ? 1 : 0)) * p.m + row;
   }
-  x.row_next = 2 * (static_cast<size_t>(c0) + 1) * PD_M + row;
+  x.row_next = 2 * (static_cast<size_t>(c0) + 1) * p.m + row;
+  x.step = 2 * p.m;
   return x;
 }
 
 __device__ __forceinline__ size_t pd_part_row(const PdParts& x, int s) {
-  return s == 0 ? x.row : x.row_next + static_cast<size_t>(s - 1) * 2 * PD_M;
+  return s == 0 ? x.row : x.row_next + static_cast<size_t>(s - 1) * x.step;
 }
 
 // Four columns of row `idx` of the output: the parts of `a`, then those of
@@ -695,28 +857,50 @@ __device__ __forceinline__ size_t pd_part_row(const PdParts& x, int s) {
 template <int D, bool BF16, bool OUT_F32>
 __device__ __forceinline__ void pd_merge_row(const PdParams& p, size_t idx, int c4, const PdParts& a,
                                              const PdParts& b) {
+  // eight parts at a time, their loads in flight together
+  constexpr int U = 8;
   const int n = a.n + b.n;
-  float mx = -INFINITY;
+  float mx = -INFINITY, tot = 0.f;
   bool nan = false;
-  for (int s = 0; s < n; ++s) {
-    const float x = s < a.n ? __ldcg(a.lse + pd_part_row(a, s)) : __ldcg(b.lse + pd_part_row(b, s - a.n));
-    nan |= x != x;
-    mx = fmaxf(mx, x);
-  }
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float tot = 0.f;
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < n; ++s) {
-    const PdParts& x = s < a.n ? a : b;
-    const size_t row = pd_part_row(x, s < a.n ? s : s - a.n);
-    const float wgt = expf(__ldcg(x.lse + row) - ref);
-    if (wgt == 0.f) continue;      // a part with no kept position, or far below the others
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(x.o + row * D) + c4);
-    tot += wgt;
-    r.x = fmaf(wgt, y.x, r.x);
-    r.y = fmaf(wgt, y.y, r.y);
-    r.z = fmaf(wgt, y.z, r.z);
-    r.w = fmaf(wgt, y.w, r.w);
+  for (int s0 = 0; s0 < n; s0 += U) {
+    float l[U];
+    float4 y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u;
+      l[u] = -INFINITY;
+      y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < n) {
+        const PdParts& x = s < a.n ? a : b;
+        const size_t row = pd_part_row(x, s < a.n ? s : s - a.n);
+        l[u] = __ldcg(x.lse + row);
+        y[u] = __ldcg(reinterpret_cast<const float4*>(x.o + row * D) + c4);
+      }
+    }
+    float m = mx;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      nan |= l[u] != l[u];
+      m = fmaxf(m, l[u]);
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float scale = expf(mx - ref);          // 0 for the first parts
+    mx = m;
+    tot *= scale;
+    r.x *= scale;
+    r.y *= scale;
+    r.z *= scale;
+    r.w *= scale;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float wgt = expf(l[u] - ref);
+      tot += wgt;
+      r.x = fmaf(wgt, y[u].x, r.x);
+      r.y = fmaf(wgt, y[u].y, r.y);
+      r.z = fmaf(wgt, y[u].z, r.z);
+      r.w = fmaf(wgt, y[u].w, r.w);
+    }
   }
   const bool none = mx == -INFINITY && !nan;
   const float inv = none ? 0.f : 1.f / tot;
@@ -730,43 +914,49 @@ __device__ __forceinline__ void pd_merge_row(const PdParams& p, size_t idx, int 
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + idx * D)[c4] =
         make_uint2(pack2<BF16>(r.x, r.y), pack2<BF16>(r.z, r.w));
   }
-  if (c4 == 0 && p.lse != nullptr) p.lse[idx] = none ? -INFINITY : ref + logf(tot);
+  if (c4 == 0 && p.lse != nullptr) p.lse[idx] = none ? -INFINITY : mx + logf(tot);
 }
 
 // Without a shared prefix: CTA c takes the group that the boundary behind
 // range c cuts, if any, and of it the share that falls to it among the
 // boundaries that cut the same group.
+//
+// Both merging kernels may read the lengths before their dependency wait: every
+// CTA of the attending kernel had passed its own when this one was launched,
+// so what ran before that kernel is complete, and it writes no lengths.
 template <int D, bool BF16, bool OUT_F32>
 __global__ void __launch_bounds__(PD_THREADS)
 attn_paged_merge(const PdParams p) {
-  __shared__ long long part[PD_WARPS], slot[2];
+  __shared__ int part[PD_WARPS + 2];
+  const int HR = p.H_kv * p.row_tiles;
+  const PdSum sum = pd_sum(p, part, nullptr);
+  const PdCut cut = pd_cut(sum.total * HR, p.ranges);
+  const int c = blockIdx.x;
+  PdWalk w;
+  bool any = c + 1 < cut.n;
+  int c_first = 0, cuts = 1, g_start = 0;
+  if (any) {
+    w.x = pd_start(cut, c + 1) - 1;
+    w.end = w.x + 1;
+    pd_locate(p, sum, w.x / HR, part, w.b, w.base);
+    w.base *= HR;
+    w.s = pd_seq(p, pd_len_of(p, w.b));
+    pd_run_here(p, w);
+    g_start = w.x - w.i0;
+    any = w.i0 + 1 < w.s.tiles;                   // else the group ends with the range
+    c_first = pd_range_of(cut, g_start);
+    cuts = pd_range_of(cut, g_start + w.s.tiles - 1) - c_first;
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  const int HR = p.H_kv * p.row_tiles;
-  const long long F = pd_total(p, part) * HR;
-  const int ranges = static_cast<int>(F < p.ranges ? F : p.ranges);
-  const int c = blockIdx.x;
-  if (c + 1 >= ranges) return;
-  PdWalk w;
-  w.x = pd_start(c + 1, F, ranges) - 1;
-  w.end = w.x + 1;
-  long long before;
-  pd_locate(p, w.x / HR, part, slot, w.b, before);
-  w.base = before * HR;
-  w.s = pd_seq(p, w.b);
-  pd_run_here(p, w);
-  const long long g_start = w.x - w.i0;
-  if (w.i0 + 1 == w.s.tiles) return;             // the group ends with the range
-  const int c_first = pd_range_of(g_start, F, ranges);
-  const int c_last = pd_range_of(g_start + w.s.tiles - 1, F, ranges);
-  const int cuts = c_last - c_first;
-  for (int x = (c - c_first) * PD_THREADS + threadIdx.x; x < PD_M * (D / 4); x += cuts * PD_THREADS) {
+  if (!any) return;
+  const int r_first = w.rt * p.m, n_rows = min(p.m, p.R - r_first);
+  const size_t idx0 = (static_cast<size_t>(w.b) * p.H + w.h * p.G) * p.N_q + r_first;
+  for (int x = (c - c_first) * PD_THREADS + threadIdx.x; x < n_rows * (D / 4); x += cuts * PD_THREADS) {
     const int r = x / (D / 4), c4 = x % (D / 4);
-    const PdRow row = pd_row(p, w, r);
-    if (!row.real) continue;
     PdParts none;
     none.n = 0;
-    pd_merge_row<D, BF16, OUT_F32>(p, row.idx, c4, pd_parts(p, g_start, w.s.tiles, F, ranges, 0, r), none);
+    pd_merge_row<D, BF16, OUT_F32>(p, idx0 + r, c4, pd_parts(p, cut, g_start, w.s.tiles, 0, r), none);
   }
 }
 
@@ -774,44 +964,34 @@ attn_paged_merge(const PdParams p) {
 template <int D, bool BF16, bool OUT_F32>
 __global__ void __launch_bounds__(PD_THREADS)
 attn_paged_merge_shared(const PdParams p, const PdParams pre) {
-  __shared__ long long part[PD_WARPS];
-  grid_dependency_wait();
-  grid_launch_dependents();
+  __shared__ int part[PD_WARPS + 2];
   const int HR = p.H_kv * p.row_tiles;
   const int g = static_cast<int>(blockIdx.x % HR), b = static_cast<int>(blockIdx.x / HR);
-  long long x = 0, before, all = 0;
+  int x = 0, all = 0, before, total;
   for (int i = threadIdx.x; i < p.B; i += PD_THREADS) {
-    const int tiles = pd_seq(p, i).tiles;
+    const int tiles = pd_seq(p, pd_len_of(p, i)).tiles;
     all += tiles;
     if (i < b) x += tiles;
   }
-  long long total;
   pd_scan(x, part, before);
   pd_scan(all, part, total);
-  const long long F = total * HR;
-  const int ranges = static_cast<int>(F < p.ranges ? F : p.ranges);
-  PdWalk w;
-  w.b = b;
-  w.s = pd_seq(p, b);
-  w.base = before * HR;
-  w.x = w.base + static_cast<long long>(g) * w.s.tiles;
-  w.end = w.x + w.s.tiles;
-  pd_run_here(p, w);
-  const long long g_start = w.x;
-  const long long pF = static_cast<long long>(pre.shared_tiles) * pre.H_kv * pre.row_tiles;
-  const int p_ranges = static_cast<int>(pF < pre.ranges ? pF : pre.ranges);
+  const PdCut cut = pd_cut(total * HR, p.ranges);
+  const PdCut p_cut = pd_cut(pre.shared_tiles * pre.H_kv * pre.row_tiles, pre.ranges);
+  const PdSeq s = pd_seq(p, pd_len_of(p, b));
+  const int g_start = before * HR + g * s.tiles;
+  const int h = g / p.row_tiles, r_first = (g - h * p.row_tiles) * p.m;
+  const int n_rows = min(p.m, p.R - r_first);
   const size_t group = static_cast<size_t>(b) * HR + g;
-  for (int i = threadIdx.x; i < PD_M * (D / 4); i += PD_THREADS) {
+  const size_t idx0 = (static_cast<size_t>(b) * p.H + h * p.G) * p.N_q + r_first;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int i = threadIdx.x; i < n_rows * (D / 4); i += PD_THREADS) {
     const int r = i / (D / 4), c4 = i % (D / 4);
-    const PdRow row = pd_row(p, w, r);
-    if (!row.real) continue;
-    const long long pr = static_cast<long long>(b) * p.R + w.rt * PD_M + r;     // row of the prefix
-    const size_t pg = static_cast<size_t>(w.h) * pre.row_tiles + pr / PD_M;
-    pd_merge_row<D, BF16, OUT_F32>(
-        p, row.idx, c4,
-        pd_parts(pre, static_cast<long long>(pg) * pre.shared_tiles, pre.shared_tiles, pF, p_ranges, pg,
-                 static_cast<int>(pr % PD_M)),
-        pd_parts(p, g_start, w.s.tiles, F, ranges, group, r));
+    const int pr = b * p.R + r_first + r;         // row of the prefix
+    const int pg = h * pre.row_tiles + pr / pre.m;
+    pd_merge_row<D, BF16, OUT_F32>(p, idx0 + r, c4,
+                                   pd_parts(pre, p_cut, pg * pre.shared_tiles, pre.shared_tiles, pg, pr % pre.m),
+                                   pd_parts(p, cut, g_start, s.tiles, group, r));
   }
 }
 

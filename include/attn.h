@@ -270,7 +270,7 @@ typedef struct attn_pages {
  *   shared_table, shared_len   the first min(shared_len, lens[b]) positions of
  *          every sequence hold the same rows, and shared_table (device,
  *          [ceil(shared_len / page_size)] int32) lists pages that hold them.
- *          Whole 128-position tiles of them are then attended once for the query rows
+ *          Whole tiles of them are then attended once for the query rows
  *          of all sequences instead of once a sequence.  It changes what is
  *          read, not what is computed: the result is that of shared_len = 0,
  *          up to rounding.  0 and NULL: nothing is shared.  With window > 0
@@ -280,8 +280,9 @@ typedef struct attn_pages {
  *          attn_decode_paged_workspace_bytes(...) bytes, 256-byte aligned;
  *          needs no initial contents, not to be shared by calls in flight at
  *          once
- *   N_q >= 0; (H / H_kv) * N_q <= 1024 (else ATTN_ERR_UNSUPPORTED); d is 64 or
- *   128; causal, window, n_sink, scale as for attn_fwd
+ *   N_q >= 0; (H / H_kv) * N_q <= 1024 and ceil((H / H_kv) * N_q / 16) * B * H_kv *
+ *   (max_pages * page_size / 64 + 1) < 2^31 (else ATTN_ERR_UNSUPPORTED); d is 64 or 128;
+ *   causal, window, n_sink, scale as for attn_fwd
  *
  * A query row keeps key j iff j < lens[b] and the mask rule of attn_fwd holds
  * with the row's position for i.  A row that keeps nothing (an empty sequence,
