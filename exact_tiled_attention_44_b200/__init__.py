@@ -64,6 +64,12 @@ EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_host", "attn_fwd_alibi", "attn_alibi_s
 
 _LIB = None
 
+# The current device and a device's current stream as an integer, without the
+# Python objects around them (2 us less a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 class AttnError(RuntimeError):
     def __init__(self, status: int, what: str = "attn_fwd"):
@@ -344,7 +350,7 @@ class PagedCache:
     All contiguous, on one device.  The tensors are read-only attributes: the
     calls change their contents, in stream order.
     """
-    __slots__ = ("_t", "_c", "_ptr")
+    __slots__ = ("_t", "_c", "_ptr", "_dev", "_need")
 
     def __init__(self, k, v, table, lens, refs=None):
         if k.dim() != 4 or v.shape != k.shape:
@@ -367,13 +373,15 @@ class PagedCache:
                                k.shape[1], k.shape[2], k.shape[3], table.shape[0], table.shape[1],
                                code)
         self._ptr = ctypes.addressof(self._c)
+        self._dev = dev
+        self._need = {}      # workspace bytes by the sizes of a call
 
     k = property(lambda self: self._t[0])
     v = property(lambda self: self._t[1])
     table = property(lambda self: self._t[2])
     lens = property(lambda self: self._t[3])
     refs = property(lambda self: self._t[4])
-    device = property(lambda self: self._t[0].device)
+    device = property(lambda self: self._dev)
 
 
 def paged_cache(B: int, max_pages: int, n_pages: int, H_kv: int, page_size: int, d: int,
@@ -406,22 +414,20 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
     the batch, with the same result.  ``workspace``: a CUDA uint8 tensor of at least
     decode_paged_workspace_bytes(...) bytes; allocated here (torch) when
     omitted.  Returns (o [B, H, N_q, d], lse [B, H, N_q] or None)."""
-    c = cache._c
+    c, dev = cache._c, cache._dev
     if q.dim() != 4:
         raise ValueError("q [B, H, N_q, d] expected")
     B, H, N_q, d = q.shape
-    dev = q.device
     if B != c.B or d != c.d:
         raise ValueError(f"shape mismatch q={tuple(q.shape)}, cache of {c.B} sequences, d={c.d}")
     if q.dtype != cache._t[0].dtype:
         raise TypeError("q and the cache must share one dtype")
-    if dev != cache._t[0].device:
+    if q.device != dev:
         raise ValueError("q and the cache must be on one device")
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
-    odt = torch.float32 if out_f32 else q.dtype
     if out is not None:
-        _expect(out, "out", (B, H, N_q, d), odt, dev)
+        _expect(out, "out", (B, H, N_q, d), torch.float32 if out_f32 else q.dtype, dev)
     if lse is not None:
         _expect(lse, "lse", (B, H, N_q), torch.float32, dev)
     if shared_table is not None:
@@ -430,43 +436,25 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
         _expect(shared_table, "shared_table", (-(-shared_len // c.page_size),), torch.int32, dev)
     if workspace is not None:
         _expect_workspace(workspace, dev)
-    if not q.is_cuda:
-        raise ValueError("decode_paged() takes CUDA tensors")
+    _on_cuda(dev, "decode_paged")
     if scale is None:
         scale = _DEFAULT_SCALE.get(d) or default_scale(d)
     if out is None:
-        out = torch.empty((B, H, N_q, d), dtype=odt, device=dev)
+        out = torch.empty_like(q, dtype=torch.float32) if out_f32 else torch.empty_like(q)
     if lse is None and return_lse:
-        lse = torch.empty((B, H, N_q), dtype=torch.float32, device=dev)
-    lib = load_library()
+        lse = q.new_empty((B, H, N_q), dtype=torch.float32)
     if workspace is None:
-        need = lib.attn_decode_paged_workspace_bytes(B, H, c.H_kv, N_q, d, shared_len)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    with _Device(dev):
-        rc = lib.attn_decode_paged(q.data_ptr(), cache._ptr, out.data_ptr(),
-                                   lse.data_ptr() if lse is not None else None,
-                                   shared_table.data_ptr() if shared_table is not None else None,
-                                   shared_len, workspace.data_ptr() if workspace is not None else None,
-                                   workspace.numel() if workspace is not None else 0, H, N_q,
-                                   int(causal), window, n_sink, scale, int(out_f32), stream)
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_decode_paged")
+        sizes = (H, N_q, shared_len)
+        need = cache._need.get(sizes)
+        if need is None:
+            need = cache._need[sizes] = decode_paged_workspace_bytes(B, H, c.H_kv, N_q, d, shared_len)
+        workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=dev)
+    _call(dev, "attn_decode_paged", q.data_ptr(), cache._ptr, out.data_ptr(),
+          lse.data_ptr() if lse is not None else None,
+          shared_table.data_ptr() if shared_table is not None else None, shared_len,
+          workspace.data_ptr(), workspace.numel(), H, N_q, int(causal), window, n_sink, scale,
+          int(out_f32))
     return out, lse
-
-
-def _managed(cache: PagedCache, what: str, **ints):
-    """The device of a cache that a pages_*() call may change; checks that the
-    named tensors are contiguous 1-D int32 tensors there."""
-    if cache._t[4] is None:
-        raise ValueError(f"{what}() needs a cache with refs")
-    dev = cache._t[0].device
-    for name, t in ints.items():
-        if t is not None and (t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous()
-                              or t.device != dev):
-            raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on {dev}")
-    return dev
 
 
 def _on_cuda(dev, what: str):
@@ -474,18 +462,40 @@ def _on_cuda(dev, what: str):
         raise ValueError(f"{what}() takes a CUDA cache")
 
 
-def _pages_call(dev, name: str, *args):
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    with _Device(dev):
-        rc = getattr(load_library(), name)(*args, stream)
+def _call(dev, name: str, *args):
+    """The C call on the current stream of `dev`, made the current device for it."""
+    fn = getattr(_LIB or load_library(), name)
+    index = dev.index
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, name)
 
 
-def _scratch(workspace, need: int, dev):
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    return workspace
+def _managed(cache: PagedCache, what: str):
+    """The device of a cache that a pages_*() call may change."""
+    if cache._t[4] is None:
+        raise ValueError(f"{what}() needs a cache with refs")
+    return cache._dev
+
+
+def _ints(t: torch.Tensor, name: str, dev):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on {dev}")
+
+
+def _scratch(workspace, cache: PagedCache, sizes, query):
+    """The caller's workspace, or one of the bytes that query() asks for."""
+    if workspace is not None:
+        _expect_workspace(workspace, cache._dev)
+        return workspace
+    need = cache._need.get(sizes)
+    if need is None:
+        need = cache._need[sizes] = max(int(query()), 16)
+    return torch.empty(need, dtype=torch.uint8, device=cache._dev)
 
 
 def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -497,21 +507,21 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     do not suffice for stay as they are; get_status() then gives
     ATTN_ERR_NO_PAGES."""
     c = cache._c
-    dev = _managed(cache, "pages_append", counts=counts)
+    dev = _managed(cache, "pages_append")
     n_new = k_new.shape[2] if k_new.dim() == 4 else -1
     shape = (c.B, c.H_kv, n_new, c.d)
     _expect(k_new, "k_new", shape, cache._t[0].dtype, dev)
     _expect(v_new, "v_new", shape, cache._t[0].dtype, dev)
-    if counts is not None and counts.shape[0] != c.B:
-        raise ValueError(f"counts must have {c.B} elements")
-    if workspace is not None:
-        _expect_workspace(workspace, dev)
+    if counts is not None:
+        _ints(counts, "counts", dev)
+        if counts.shape[0] != c.B:
+            raise ValueError(f"counts must have {c.B} elements")
     _on_cuda(dev, "pages_append")
-    workspace = _scratch(workspace, load_library().attn_pages_append_workspace_bytes(
-        c.B, n_new, c.page_size), dev)
-    _pages_call(dev, "attn_pages_append", cache._ptr, k_new.data_ptr(), v_new.data_ptr(),
-                counts.data_ptr() if counts is not None else None, n_new, workspace.data_ptr(),
-                workspace.numel())
+    workspace = _scratch(workspace, cache, ("append", n_new),
+                         lambda: load_library().attn_pages_append_workspace_bytes(c.B, n_new, c.page_size))
+    _call(dev, "attn_pages_append", cache._ptr, k_new.data_ptr(), v_new.data_ptr(),
+          counts.data_ptr() if counts is not None else None, n_new, workspace.data_ptr(),
+          workspace.numel())
 
 
 def pages_trim(cache: PagedCache, new_lens: torch.Tensor | None = None,
@@ -520,30 +530,35 @@ def pages_trim(cache: PagedCache, new_lens: torch.Tensor | None = None,
     releases the pages behind (attn_pages_trim).  ``rows``: int32 row numbers;
     default rows 0, 1, ... (all of them when new_lens is None too)."""
     c = cache._c
-    dev = _managed(cache, "pages_trim", new_lens=new_lens, rows=rows)
+    dev = _managed(cache, "pages_trim")
     n = c.B
     if rows is not None:
+        _ints(rows, "rows", dev)
         n = rows.shape[0]
-    elif new_lens is not None:
-        n = new_lens.shape[0]
-    if new_lens is not None and new_lens.shape[0] != n:
-        raise ValueError("new_lens and rows must be of one length")
-    if rows is None and n > c.B:
-        raise ValueError(f"new_lens has {n} elements for {c.B} sequences")
+    if new_lens is not None:
+        _ints(new_lens, "new_lens", dev)
+        if rows is None:
+            n = new_lens.shape[0]
+            if n > c.B:
+                raise ValueError(f"new_lens has {n} elements for {c.B} sequences")
+        elif new_lens.shape[0] != n:
+            raise ValueError("new_lens and rows must be of one length")
     _on_cuda(dev, "pages_trim")
-    _pages_call(dev, "attn_pages_trim", cache._ptr, rows.data_ptr() if rows is not None else None,
-                new_lens.data_ptr() if new_lens is not None else None, n)
+    _call(dev, "attn_pages_trim", cache._ptr, rows.data_ptr() if rows is not None else None,
+          new_lens.data_ptr() if new_lens is not None else None, n)
 
 
 def pages_fork(cache: PagedCache, parents: torch.Tensor, children: torch.Tensor) -> None:
     """Makes the empty row children[i] a copy of row parents[i] that shares its
     pages (attn_pages_fork); int32 tensors of one length."""
-    dev = _managed(cache, "pages_fork", parents=parents, children=children)
+    dev = _managed(cache, "pages_fork")
+    _ints(parents, "parents", dev)
+    _ints(children, "children", dev)
     if parents.shape != children.shape:
         raise ValueError("parents and children must be of one length")
     _on_cuda(dev, "pages_fork")
-    _pages_call(dev, "attn_pages_fork", cache._ptr, parents.data_ptr(), children.data_ptr(),
-                parents.shape[0])
+    _call(dev, "attn_pages_fork", cache._ptr, parents.data_ptr(), children.data_ptr(),
+          parents.shape[0])
 
 
 def pages_compact(cache: PagedCache, *, table_out: torch.Tensor | None = None,
@@ -561,27 +576,28 @@ def pages_compact(cache: PagedCache, *, table_out: torch.Tensor | None = None,
         _expect(refs_out, "refs_out", (c.n_pages,), torch.int32, dev)
     if n_live is not None:
         _expect(n_live, "n_live", (1,), torch.int32, dev)
-    if workspace is not None:
-        _expect_workspace(workspace, dev)
     _on_cuda(dev, "pages_compact")
     if n_live is None:
         n_live = torch.empty(1, dtype=torch.int32, device=dev)
-    workspace = _scratch(workspace, load_library().attn_pages_compact_workspace_bytes(c.n_pages), dev)
-    _pages_call(dev, "attn_pages_compact", cache._ptr,
-                table_out.data_ptr() if table_out is not None else None,
-                refs_out.data_ptr() if refs_out is not None else None, n_live.data_ptr(),
-                workspace.data_ptr(), workspace.numel())
+    workspace = _scratch(workspace, cache, "compact",
+                         lambda: load_library().attn_pages_compact_workspace_bytes(c.n_pages))
+    _call(dev, "attn_pages_compact", cache._ptr,
+          table_out.data_ptr() if table_out is not None else None,
+          refs_out.data_ptr() if refs_out is not None else None, n_live.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return n_live
 
 
 def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor) -> None:
     """Copies page src[i]'s K and V rows to page dst[i] (attn_pages_copy); int32
     tensors of one length, entries with src[i] < 0 are skipped."""
-    dev = _managed(cache, "pages_copy", src=src, dst=dst)
+    dev = _managed(cache, "pages_copy")
+    _ints(src, "src", dev)
+    _ints(dst, "dst", dev)
     if src.shape != dst.shape:
         raise ValueError("src and dst must be of one length")
     _on_cuda(dev, "pages_copy")
-    _pages_call(dev, "attn_pages_copy", cache._ptr, src.data_ptr(), dst.data_ptr(), src.shape[0])
+    _call(dev, "attn_pages_copy", cache._ptr, src.data_ptr(), dst.data_ptr(), src.shape[0])
 
 
 def bwd_workspace_bytes(B: int, H: int, N: int, d: int, dtype: int) -> int:

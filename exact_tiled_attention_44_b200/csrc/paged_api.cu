@@ -1,16 +1,32 @@
 // paged_api.cu -- the decoding step over a K/V cache of pages:
 // attn_decode_paged and its workspace query.
 #include "host.h"
-#include "paged_kernel.cuh"
+#include "paged_tc_kernel.cuh"
 
 namespace attn_host {
 
 namespace {
 
-// Ranges of the tile space (two CTAs on each SM of a B200); fixed, so that the
-// workspace can be sized without a device.
-constexpr int kPagedRanges = 296;
 constexpr int kPagedMaxRows = 1024;   // (H / H_kv) * N_q
+constexpr int kSharedUnit = 128;      // the shared prefix is attended in whole tiles of this many positions
+
+// How the `rows` query rows of a sequence (or, in a shared prefix, of the
+// batch) and K/V head are attended: rows of a group, groups, positions of a
+// tile, ranges of the tile space.  The ranges are one CTA (of
+// attn_paged_tc_kernel) or two (of attn_paged_kernel) on each SM of a B200;
+// fixed, so that the workspace can be sized without a device.
+struct PagedForm {
+  int m, row_tiles, tile_shift, ranges;
+};
+
+PagedForm paged_form(long long rows) {
+  PagedForm f;
+  f.m = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+  f.row_tiles = static_cast<int>((rows + f.m - 1) / f.m);
+  f.tile_shift = f.m <= 16 ? 6 : 7;
+  f.ranges = f.m <= 16 ? 296 : 148;
+  return f;
+}
 
 // Workspace of one attending launch over `groups` groups: two slots a range
 // for the runs of split groups, and, behind or of a shared prefix, one result
@@ -19,8 +35,8 @@ struct PagedSpace {
   size_t part_o, part_lse, own_o, own_lse, end;
 };
 
-PagedSpace paged_space(size_t at, size_t groups, int m, int d) {
-  const size_t rows = size_t(2) * kPagedRanges * m, own = groups * m;
+PagedSpace paged_space(size_t at, const PagedForm& f, size_t groups, int d) {
+  const size_t rows = size_t(2) * f.ranges * f.m, own = groups * f.m;
   PagedSpace s;
   s.part_o = at;
   s.part_lse = s.part_o + rows * d * 4;
@@ -32,8 +48,7 @@ PagedSpace paged_space(size_t at, size_t groups, int m, int d) {
 
 struct PagedPlan {
   bool shared;
-  int m, row_tiles;                // rows of a group, and groups of a sequence's rows
-  int prefix_m, prefix_tiles;      // the same of the batch's rows
+  PagedForm form, prefix_form;
   PagedSpace own, prefix;
   size_t bytes;
 };
@@ -41,16 +56,13 @@ struct PagedPlan {
 PagedPlan paged_plan(int B, int H, int H_kv, int N_q, int d, int shared_len) {
   PagedPlan pl{};
   const long long R = static_cast<long long>(H / H_kv) * N_q;
-  pl.shared = shared_len >= attn::PD_TILE;
-  pl.m = R <= 8 ? 8 : 16;
-  pl.row_tiles = static_cast<int>((R + pl.m - 1) / pl.m);
-  pl.prefix_m = B * R <= 8 ? 8 : 16;
-  pl.prefix_tiles = static_cast<int>((B * R + pl.prefix_m - 1) / pl.prefix_m);
-  const size_t groups = static_cast<size_t>(B) * H_kv * pl.row_tiles;
-  pl.own = paged_space(0, pl.shared ? groups : 0, pl.m, d);
+  pl.shared = shared_len >= kSharedUnit;
+  pl.form = paged_form(R);
+  pl.own = paged_space(0, pl.form, pl.shared ? static_cast<size_t>(B) * H_kv * pl.form.row_tiles : 0, d);
   pl.bytes = pl.own.end;
   if (pl.shared) {
-    pl.prefix = paged_space(pl.own.end, static_cast<size_t>(H_kv) * pl.prefix_tiles, pl.prefix_m, d);
+    pl.prefix_form = paged_form(B * R);
+    pl.prefix = paged_space(pl.own.end, pl.prefix_form, static_cast<size_t>(H_kv) * pl.prefix_form.row_tiles, d);
     pl.bytes = pl.prefix.end;
   }
   return pl;
@@ -72,42 +84,85 @@ int encode_pages(CUtensorMap* map, const void* base, bool bf16, int d, int page_
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// 3-D view [z][page_size][d] of the same; a box is as many rows of 64 columns
+// as a page and a tile of attn_paged_tc_kernel have in common.
+int encode_boxes(CUtensorMap* map, const void* base, bool bf16, int d, int page_size, int z) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(z)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(page_size) * d * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(page_size < attn::PT_TILE ? page_size : attn::PT_TILE), 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 int counted(cudaError_t e) {
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-template <int D, int NT, bool BF16, bool F32>
-int launch_attend(DeviceState* st, const attn::PdParams& dp, const CUtensorMap& mk, const CUtensorMap& mv,
-                  cudaStream_t stream) {
-  auto kern = attn::attn_paged_kernel<D, NT, BF16, F32>;
-  const int smem = attn::PdGeo<D, NT>::SMEM_BYTES + 1024;
-  const uint32_t bit = 1u << ((D == 128 ? 8 : 0) + (NT == 2 ? 4 : 0) + (BF16 ? 2 : 0) + (F32 ? 1 : 0));
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (!(st->paged_attr_set & bit)) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return ATTN_ERR_CUDA;
-      st->paged_attr_set |= bit;
-    }
+// Sets a kernel's shared memory on its first launch on the device; `regs`:
+// the registers a thread it has to be launched with (it re-splits them).
+template <typename Kern>
+int prepare_kernel(DeviceState* st, Kern kern, uint32_t bit, int smem, int regs) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (st->paged_attr_set & bit) return ATTN_OK;
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (fa.numRegs < regs) return ATTN_ERR_UNSUPPORTED;
   }
-  return counted(launch_overlapped(kern, dp.ranges, attn::PD_THREADS, smem, stream, mk, mv, dp));
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  st->paged_attr_set |= bit;
+  return ATTN_OK;
+}
+
+// One attending launch: the kernel for dp.m query rows a group.
+template <int D, bool BF16, bool F32>
+int attend(DeviceState* st, const attn::PdParams& dp, const attn_pages_t* kv, cudaStream_t stream) {
+  alignas(64) CUtensorMap mk, mv;
+  const int z = dp.n_pages * dp.H_kv;
+  const auto encode = dp.m <= 16 ? encode_pages : encode_boxes;
+  if (encode(&mk, kv->k, BF16, D, kv->page_size, z) != ATTN_OK ||
+      encode(&mv, kv->v, BF16, D, kv->page_size, z) != ATTN_OK)
+    return ATTN_ERR_CUDA;
+  const auto go = [&](auto kern, int form, int smem, int regs, int threads) {
+    const uint32_t bit = 1u << (form * 8 + (D == 128 ? 4 : 0) + (BF16 ? 2 : 0) + (F32 ? 1 : 0));
+    const int rc = prepare_kernel(st, kern, bit, smem, regs);
+    if (rc != ATTN_OK) return rc;
+    return counted(launch_overlapped(kern, dp.ranges, threads, smem, stream, mk, mv, dp));
+  };
+  switch (dp.m) {
+    case 8:
+      return go(attn::attn_paged_kernel<D, 1, BF16, F32>, 0, attn::PdGeo<D, 1>::SMEM_BYTES + 1024, 0, attn::PD_THREADS);
+    case 16:
+      return go(attn::attn_paged_kernel<D, 2, BF16, F32>, 1, attn::PdGeo<D, 2>::SMEM_BYTES + 1024, 0, attn::PD_THREADS);
+    case 128:
+      return go(attn::attn_paged_tc_kernel<D, false, BF16, F32>, 2, attn::PtGeo<D, false>::SMEM_BYTES + 1024,
+                attn::LAUNCH_REGS, attn::NUM_THREADS);
+    default:
+      return go(attn::attn_paged_tc_kernel<D, true, BF16, F32>, 3, attn::PtGeo<D, true>::SMEM_BYTES + 1024,
+                attn::LAUNCH_REGS, attn::NUM_THREADS);
+  }
 }
 
 template <int D, bool BF16, bool F32>
-int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams* pre, const CUtensorMap& mk,
-                 const CUtensorMap& mv, cudaStream_t stream) {
-  const auto attend = [&](const attn::PdParams& x) {
-    return x.m == 8 ? launch_attend<D, 1, BF16, F32>(st, x, mk, mv, stream)
-                    : launch_attend<D, 2, BF16, F32>(st, x, mk, mv, stream);
-  };
+int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams* pre, const attn_pages_t* kv,
+                 cudaStream_t stream) {
   int rc = ATTN_OK;
-  if (pre != nullptr) rc = attend(*pre);
-  if (rc == ATTN_OK) rc = attend(dp);
+  if (pre != nullptr) rc = attend<D, BF16, F32>(st, *pre, kv, stream);
+  if (rc == ATTN_OK) rc = attend<D, BF16, F32>(st, dp, kv, stream);
   if (rc != ATTN_OK) return rc;
-  if (pre != nullptr)
-    return counted(launch_overlapped(attn::attn_paged_merge_shared<D, BF16, F32>, dp.B * dp.H_kv * dp.row_tiles,
+  if (pre != nullptr) {
+    // a CTA for as many rows as it takes at once, four CTAs on an SM at most
+    const int at_once = attn::PD_THREADS / (D / 4), rows = dp.B * dp.H * dp.N_q;
+    const int grid = (rows + at_once - 1) / at_once;
+    return counted(launch_overlapped(attn::attn_paged_merge_shared<D, BF16, F32>, grid < 592 ? grid : 592,
                                      attn::PD_THREADS, 0, stream, dp, *pre));
+  }
   return counted(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges, attn::PD_THREADS, 0, stream, dp));
 }
 
@@ -173,11 +228,6 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   rc = device_state(&st);
   if (rc != ATTN_OK) return rc;
   const bool bf16 = kv->dtype == ATTN_BF16;
-  alignas(64) CUtensorMap mk, mv;
-  const int z = kv->n_pages * H_kv;
-  if (encode_pages(&mk, kv->k, bf16, d, kv->page_size, z) != ATTN_OK ||
-      encode_pages(&mv, kv->v, bf16, d, kv->page_size, z) != ATTN_OK)
-    return ATTN_ERR_CUDA;
   attn::PdParams dp{};
   dp.q = q;
   dp.o = o;
@@ -200,44 +250,43 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   dp.scale_log2 = scale * 1.4426950408889634f;
   dp.G = H / H_kv;
   dp.R = static_cast<int>(R);
-  dp.m = pl.m;
-  dp.row_tiles = pl.row_tiles;
-  dp.ranges = kPagedRanges;
   dp.withhold_loads = take_withhold();
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const auto place = [&](attn::PdParams& x, const PagedSpace& s) {
+  const auto place = [&](attn::PdParams& x, const PagedForm& f, const PagedSpace& s) {
+    x.m = f.m;
+    x.row_tiles = f.row_tiles;
+    x.tile_shift = f.tile_shift;
+    x.ranges = f.ranges;
     x.part_o = reinterpret_cast<float*>(ws + s.part_o);
     x.part_lse = reinterpret_cast<float*>(ws + s.part_lse);
     x.own_o = reinterpret_cast<float*>(ws + s.own_o);
     x.own_lse = reinterpret_cast<float*>(ws + s.own_lse);
   };
-  place(dp, pl.own);
+  place(dp, pl.form, pl.own);
   attn::PdParams pre = dp;
   // whole tiles of the prefix are attended once; a window moves with each
   // row, so under one every sequence reads its own pages
-  const int shared_tiles = static_cast<int>((shared_len < cap ? shared_len : cap) / attn::PD_TILE);
-  const bool shared = shared_tiles > 0 && dp.window == 0;
+  const int units = static_cast<int>((shared_len < cap ? shared_len : cap) / kSharedUnit);
+  const bool shared = units > 0 && dp.window == 0;
   if (shared) {
-    dp.shared_tiles = shared_tiles;
-    pre.shared_tiles = dp.shared_tiles;
     pre.prefix = 1;
     pre.table = shared_table;
-    pre.m = pl.prefix_m;
-    pre.row_tiles = pl.prefix_tiles;
-    place(pre, pl.prefix);
+    place(pre, pl.prefix_form, pl.prefix);
+    pre.shared_tiles = (units * kSharedUnit) >> pre.tile_shift;
+    dp.shared_tiles = (units * kSharedUnit) >> dp.tile_shift;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const attn::PdParams* pp = shared ? &pre : nullptr;
   if (d == 128) {
-    if (bf16) return out_f32 ? launch_paged<128, true, true>(st, dp, pp, mk, mv, s)
-                             : launch_paged<128, true, false>(st, dp, pp, mk, mv, s);
-    return out_f32 ? launch_paged<128, false, true>(st, dp, pp, mk, mv, s)
-                   : launch_paged<128, false, false>(st, dp, pp, mk, mv, s);
+    if (bf16) return out_f32 ? launch_paged<128, true, true>(st, dp, pp, kv, s)
+                             : launch_paged<128, true, false>(st, dp, pp, kv, s);
+    return out_f32 ? launch_paged<128, false, true>(st, dp, pp, kv, s)
+                   : launch_paged<128, false, false>(st, dp, pp, kv, s);
   }
-  if (bf16) return out_f32 ? launch_paged<64, true, true>(st, dp, pp, mk, mv, s)
-                           : launch_paged<64, true, false>(st, dp, pp, mk, mv, s);
-  return out_f32 ? launch_paged<64, false, true>(st, dp, pp, mk, mv, s)
-                 : launch_paged<64, false, false>(st, dp, pp, mk, mv, s);
+  if (bf16) return out_f32 ? launch_paged<64, true, true>(st, dp, pp, kv, s)
+                           : launch_paged<64, true, false>(st, dp, pp, kv, s);
+  return out_f32 ? launch_paged<64, false, true>(st, dp, pp, kv, s)
+                 : launch_paged<64, false, false>(st, dp, pp, kv, s);
 }
 
 }  // extern "C"

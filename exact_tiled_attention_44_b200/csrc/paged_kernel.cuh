@@ -51,7 +51,8 @@ struct PdParams {
   float scale_log2;     // scale * log2(e)
   int G;                // H / H_kv
   int R;                // G * N_q query rows of a sequence and K/V head
-  int m;                // query rows of a group: 8 or 16
+  int m;                // query rows of a group: 8 or 16, or (paged_tc_kernel.cuh) 128 or 256
+  int tile_shift;       // log2 of the positions of a tile
   int row_tiles;        // groups of a sequence and K/V head (prefix: of a K/V head)
   int shared_tiles;     // whole tiles of the shared prefix
   int prefix;           // this launch attends the shared prefix
@@ -94,33 +95,49 @@ struct PdGeo {
 struct PdSeq {
   int len;      // positions (clamped to the table)
   int sb, w0;   // tiles [0, sb), then [w0, ...)
-  int tiles;    // at least 1, so that every group has a run
+  int tiles;    // 0: nothing is kept (of the sequence's own positions)
 };
 
 __device__ __forceinline__ int pd_len_of(const PdParams& p, int b) {
   return min(max(p.lens[b], 0), p.max_pages << p.page_shift);
 }
 
+// The same, from the lengths kept in shared memory (if there are any).
+__device__ __forceinline__ int pd_len_of(const PdParams& p, int b, const int* lens_s) {
+  return lens_s != nullptr && b < PD_LENS ? lens_s[b] : pd_len_of(p, b);
+}
+
 __device__ __forceinline__ PdSeq pd_seq(const PdParams& p, int len) {
   PdSeq s;
   if (p.prefix) {
-    s.len = p.shared_tiles * PD_TILE;
+    s.len = p.shared_tiles << p.tile_shift;
     s.sb = 0;
     s.w0 = 0;
     s.tiles = p.shared_tiles;
     return s;
   }
   s.len = len;
-  const int nt = (len + PD_TILE - 1) / PD_TILE;
+  const int tile = 1 << p.tile_shift;
+  const int nt = (len + tile - 1) >> p.tile_shift;
   s.sb = 0;
   s.w0 = p.shared_tiles;
   if (p.window > 0) {
     const int first = len - p.N_q - p.window + 1;      // both below 2^30 + 1024
-    s.sb = min((min(p.n_sink, len) + PD_TILE - 1) / PD_TILE, nt);
-    s.w0 = max(first > 0 ? first / PD_TILE : 0, s.sb);
+    s.sb = min((min(p.n_sink, len) + tile - 1) >> p.tile_shift, nt);
+    s.w0 = max(first > 0 ? first >> p.tile_shift : 0, s.sb);
   }
-  s.tiles = max(1, s.sb + max(0, nt - s.w0));
+  s.tiles = s.sb + max(0, nt - s.w0);
   return s;
+}
+
+// Lengths that do not fit the table are reported once.
+template <int THREADS>
+__device__ __forceinline__ void pd_report_lens(const PdParams& p) {
+  if (blockIdx.x != 0) return;
+  for (int b = threadIdx.x; b < p.B; b += THREADS) {
+    const int n = p.lens[b];
+    if (n < 0 || n > (p.max_pages << p.page_shift)) atomicCAS(p.status, 0, -1);
+  }
 }
 
 // F tiles in `n` ranges: the first `more` ranges have one tile more than the
@@ -132,7 +149,7 @@ struct PdCut {
 __device__ __forceinline__ PdCut pd_cut(int F, int n) {
   PdCut c;
   c.n = min(F, n);
-  c.each = F / c.n;
+  c.each = F / max(c.n, 1);
   c.more = F - c.each * c.n;
   return c;
 }
@@ -145,7 +162,9 @@ __device__ __forceinline__ int pd_range_of(const PdCut& c, int f) {
   return f < t ? f / (c.each + 1) : c.more + (f - t) / c.each;
 }
 
-// The sum of x over the CTA's PD_THREADS threads before this one, and of all.
+// The sum of x over the CTA's THREADS threads before this one, and of all.
+// `part` holds THREADS / 32 + 2 ints of shared memory.
+template <int THREADS>
 __device__ __forceinline__ int pd_scan(int x, int* part, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = x;
@@ -159,7 +178,7 @@ __device__ __forceinline__ int pd_scan(int x, int* part, int& total) {
   int before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < PD_WARPS; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     const int y = part[w];
     before += w < warp ? y : 0;
     total += y;
@@ -169,7 +188,7 @@ __device__ __forceinline__ int pd_scan(int x, int* part, int& total) {
 }
 
 // The tiles of all sequences (of one group of each) in order.  Every thread
-// holds one of the first PD_THREADS sequences; beyond them, the sums are made
+// holds one of the first THREADS sequences; beyond them, the sums are made
 // again when a tile is located.
 struct PdSum {
   int total;
@@ -177,34 +196,36 @@ struct PdSum {
 };
 
 // Also keeps the first PD_LENS lengths in shared memory when `lens_s` is given.
+template <int THREADS>
 __device__ __forceinline__ PdSum pd_sum(const PdParams& p, int* part, int* lens_s) {
   PdSum s;
   s.total = p.shared_tiles;
   s.before = 0;
   s.tiles = 0;
   int rest = 0;
-  for (int b = threadIdx.x; b < p.B; b += PD_THREADS) {
+  for (int b = threadIdx.x; b < p.B; b += THREADS) {
     const int len = pd_len_of(p, b);
     if (lens_s != nullptr && b < PD_LENS) lens_s[b] = len;
     const int tiles = pd_seq(p, len).tiles;
-    if (b < PD_THREADS) s.tiles = tiles;
+    if (b < THREADS) s.tiles = tiles;
     else rest += tiles;
   }
   if (p.prefix) {
     __syncthreads();
     return s;
   }
-  s.before = pd_scan(s.tiles, part, s.total);
-  if (p.B > PD_THREADS) {
+  s.before = pd_scan<THREADS>(s.tiles, part, s.total);
+  if (p.B > THREADS) {
     int more;
-    pd_scan(rest, part, more);
+    pd_scan<THREADS>(rest, part, more);
     s.total += more;
   }
   return s;
 }
 
 // The sequence that holds tile u of the sum of the sequences' tiles, and the
-// tiles before it.  part[PD_WARPS] and [PD_WARPS + 1] pass them on.
+// tiles before it.  The last two ints of `part` pass them on.
+template <int THREADS>
 __device__ __forceinline__ void pd_locate(const PdParams& p, const PdSum& sum, int u, int* part, int& b_out,
                                           int& before_out) {
   b_out = 0;
@@ -213,13 +234,13 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, const PdSum& sum, i
   int before = sum.before, tiles = sum.tiles, carry = 0;
   for (int b0 = 0;;) {
     if (before <= u && u < before + tiles) {
-      part[PD_WARPS] = b0 + threadIdx.x;
-      part[PD_WARPS + 1] = before;
+      part[THREADS / 32] = b0 + threadIdx.x;
+      part[THREADS / 32 + 1] = before;
     }
-    b0 += PD_THREADS;
+    b0 += THREADS;
     if (b0 >= p.B) break;
     // the sum up to this chunk is the last thread's
-    if (threadIdx.x == PD_THREADS - 1) part[0] = before + tiles;
+    if (threadIdx.x == THREADS - 1) part[0] = before + tiles;
     __syncthreads();
     carry = part[0];
     __syncthreads();
@@ -227,11 +248,11 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, const PdSum& sum, i
     const int b = b0 + threadIdx.x;
     tiles = b < p.B ? pd_seq(p, pd_len_of(p, b)).tiles : 0;
     int total;
-    before = carry + pd_scan(tiles, part, total);
+    before = carry + pd_scan<THREADS>(tiles, part, total);
   }
   __syncthreads();
-  b_out = part[PD_WARPS];
-  before_out = part[PD_WARPS + 1];
+  b_out = part[THREADS / 32];
+  before_out = part[THREADS / 32 + 1];
 }
 
 // A CTA's place in its range: the current run (tiles [i0, i_end) of group (b,
@@ -253,7 +274,8 @@ __device__ __forceinline__ void pd_run_here(const PdParams& p, PdWalk& w) {
   w.i_end = min(w.i0 + w.end - w.x, w.s.tiles);
 }
 
-// The next run of the range, if there is one; it begins a group.
+// The next run of the range, if there is one; it begins a group (of the next
+// sequence that has tiles).
 __device__ __forceinline__ bool pd_next_run(const PdParams& p, PdWalk& w, const int* lens_s) {
   w.x += w.i_end - w.i0;
   if (w.x >= w.end) return false;
@@ -263,12 +285,19 @@ __device__ __forceinline__ bool pd_next_run(const PdParams& p, PdWalk& w, const 
     if (++w.h == p.H_kv) {
       w.h = 0;
       w.base = w.x;
-      ++w.b;
-      w.s = pd_seq(p, w.b < PD_LENS ? lens_s[w.b] : pd_len_of(p, w.b));
+      do {
+        ++w.b;
+        w.s = pd_seq(p, pd_len_of(p, w.b, lens_s));
+      } while (w.s.tiles == 0);
     }
   }
   w.i_end = min(w.end - w.x, w.s.tiles);
   return true;
+}
+
+// First position of tile i.
+__device__ __forceinline__ int pd_tile_key(const PdParams& p, const PdSeq& s, int i) {
+  return (i < s.sb ? i : s.w0 + (i - s.sb)) << p.tile_shift;
 }
 
 // First position of warp `warp`'s slice of tile i.
@@ -282,10 +311,10 @@ __device__ __forceinline__ int pd_stop(const PdWalk& w, int warp) {
   return min(w.i_end, t > w.s.w0 ? w.s.sb + t - w.s.w0 : min(w.s.sb, t));
 }
 
-// Under a window, whether no row of the sequence keeps a position of the slice
-// at key0: it is neither loaded nor looked up in the table.
-__device__ __forceinline__ bool pd_gone(const PdParams& p, const PdSeq& s, int key0) {
-  return p.window > 0 && key0 >= p.n_sink && key0 + PD_SLICE - 1 < s.len - p.N_q - p.window + 1;
+// Under a window, whether no row of the sequence keeps one of the n positions
+// from key0 on: they are neither loaded nor looked up in the table.
+__device__ __forceinline__ bool pd_gone(const PdParams& p, const PdSeq& s, int key0, int n = PD_SLICE) {
+  return p.window > 0 && key0 >= p.n_sink && key0 + n - 1 < s.len - p.N_q - p.window + 1;
 }
 
 // ------------------------------------------------------------ warp pieces
@@ -350,7 +379,7 @@ __device__ __forceinline__ void pd_row_keeps(const PdParams& p, const PdWalk& w,
   if (p.prefix) {
     const int b = r / p.R;
     r -= b * p.R;
-    len = b < PD_LENS ? lens_s[b] : pd_len_of(p, b);
+    len = pd_len_of(p, b, lens_s);
   }
   const int pos = len - p.N_q + (p.N_q == 1 ? 0 : r % p.N_q);
   hi = p.causal ? pos : len - 1;
@@ -404,16 +433,16 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   __syncthreads();
 
   const int HR = p.H_kv * p.row_tiles;
-  const PdSum sum = pd_sum(p, part, lens_s);
+  const PdSum sum = pd_sum<PD_THREADS>(p, part, lens_s);
   const PdCut cut = pd_cut(sum.total * HR, gridDim.x);
   if (static_cast<int>(blockIdx.x) >= cut.n) return;
   PdWalk w;
   const int f0 = pd_start(cut, blockIdx.x);
   w.x = f0;
   w.end = pd_start(cut, blockIdx.x + 1);
-  pd_locate(p, sum, w.x / HR, part, w.b, w.base);
+  pd_locate<PD_THREADS>(p, sum, w.x / HR, part, w.b, w.base);
   w.base *= HR;
-  w.s = pd_seq(p, w.b < PD_LENS ? lens_s[w.b] : pd_len_of(p, w.b));
+  w.s = pd_seq(p, pd_len_of(p, w.b, lens_s));
   pd_run_here(p, w);
 
   // ---- this warp's loads: the slice to load next.  Lane l looks up the page of
@@ -501,13 +530,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int s = 0; s < T::NST; ++s) refill();
     store_q(x);
   }
-  // lengths that do not fit the table are reported once
-  if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < p.B; b += PD_THREADS) {
-      const int n = p.lens[b];
-      if (n < 0 || n > (p.max_pages << p.page_shift)) atomicCAS(p.status, 0, -1);
-    }
-  }
+  pd_report_lens<PD_THREADS>(p);
   __syncthreads();
 
   // Fragments: lane 4 g + t holds positions g and g + 8 (of K's slice) or
@@ -831,6 +854,8 @@ struct PdParts {
 __device__ __forceinline__ PdParts pd_parts(const PdParams& p, const PdCut& cut, int start, int tiles,
                                             size_t group, int row) {
   PdParts x;
+  x.n = 0;
+  if (tiles == 0) return x;
   const int c0 = pd_range_of(cut, start), c1 = pd_range_of(cut, start + tiles - 1);
   x.n = c1 - c0 + 1;
   if (x.n == 1) {
@@ -852,69 +877,111 @@ __device__ __forceinline__ size_t pd_part_row(const PdParts& x, int s) {
   return s == 0 ? x.row : x.row_next + static_cast<size_t>(s - 1) * x.step;
 }
 
-// Four columns of row `idx` of the output: the parts of `a`, then those of
-// `b` (b.n may be 0), weighted by exp(LSE_s - max LSE).
-template <int D, bool BF16, bool OUT_F32>
-__device__ __forceinline__ void pd_merge_row(const PdParams& p, size_t idx, int c4, const PdParts& a,
-                                             const PdParts& b) {
-  // eight parts at a time, their loads in flight together
+// A weighted sum of parts: max LSE_s, sum_s exp(LSE_s - max) and the same of
+// four columns of O_s.
+struct PdMix {
+  float top, tot;
+  float4 r;
+};
+
+__device__ __forceinline__ PdMix pd_no_parts() { return {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)}; }
+
+__device__ __forceinline__ void pd_scale(PdMix& x, float f) {
+  x.tot *= f;
+  x.r.x *= f;
+  x.r.y *= f;
+  x.r.z *= f;
+  x.r.w *= f;
+}
+
+// Parts first, first + step, ... of `a`, then of `b` (b.n may be 0), of the
+// columns 4 c4 .. 4 c4 + 3.  Eight parts' loads are in flight together.
+template <int D>
+__device__ __forceinline__ PdMix pd_mix(int c4, const PdParts& a, const PdParts& b, int first, int step) {
   constexpr int U = 8;
   const int n = a.n + b.n;
-  float mx = -INFINITY, tot = 0.f;
-  bool nan = false;
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += U) {
+  PdMix x = pd_no_parts();
+  for (int s0 = first; s0 < n; s0 += U * step) {
     float l[U];
     float4 y[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int s = s0 + u;
+      const int s = s0 + u * step;
       l[u] = -INFINITY;
       y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s < n) {
-        const PdParts& x = s < a.n ? a : b;
-        const size_t row = pd_part_row(x, s < a.n ? s : s - a.n);
-        l[u] = __ldcg(x.lse + row);
-        y[u] = __ldcg(reinterpret_cast<const float4*>(x.o + row * D) + c4);
+        const PdParts& part = s < a.n ? a : b;
+        const size_t row = pd_part_row(part, s < a.n ? s : s - a.n);
+        l[u] = __ldcg(part.lse + row);
+        y[u] = __ldcg(reinterpret_cast<const float4*>(part.o + row * D) + c4);
       }
     }
-    float m = mx;
+    float top = x.top;
+    bool nan = top != top;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       nan |= l[u] != l[u];
-      m = fmaxf(m, l[u]);
+      top = fmaxf(top, l[u]);
     }
-    const float ref = m == -INFINITY ? 0.f : m;
-    const float scale = expf(mx - ref);          // 0 for the first parts
-    mx = m;
-    tot *= scale;
-    r.x *= scale;
-    r.y *= scale;
-    r.z *= scale;
-    r.w *= scale;
+    if (nan) top = NAN;                          // kept as the maximum, it reaches all that follows
+    const float ref = top == -INFINITY ? 0.f : top;
+    pd_scale(x, expf(x.top - ref));              // 0 for the first parts
+    x.top = top;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float wgt = expf(l[u] - ref);
-      tot += wgt;
-      r.x = fmaf(wgt, y[u].x, r.x);
-      r.y = fmaf(wgt, y[u].y, r.y);
-      r.z = fmaf(wgt, y[u].z, r.z);
-      r.w = fmaf(wgt, y[u].w, r.w);
+      x.tot += wgt;
+      x.r.x = fmaf(wgt, y[u].x, x.r.x);
+      x.r.y = fmaf(wgt, y[u].y, x.r.y);
+      x.r.z = fmaf(wgt, y[u].z, x.r.z);
+      x.r.w = fmaf(wgt, y[u].w, x.r.w);
     }
   }
-  const bool none = mx == -INFINITY && !nan;
-  const float inv = none ? 0.f : 1.f / tot;
-  r.x *= inv;
-  r.y *= inv;
-  r.z *= inv;
-  r.w *= inv;
+  return x;
+}
+
+// x += y, both sums over parts.
+__device__ __forceinline__ void pd_join(PdMix& x, PdMix y) {
+  const float top = x.top != x.top || y.top != y.top ? NAN : fmaxf(x.top, y.top);
+  const float ref = top == -INFINITY ? 0.f : top;
+  pd_scale(x, expf(x.top - ref));
+  pd_scale(y, expf(y.top - ref));
+  x.top = top;
+  x.tot += y.tot;
+  x.r.x += y.r.x;
+  x.r.y += y.r.y;
+  x.r.z += y.r.z;
+  x.r.w += y.r.w;
+}
+
+// Row `idx` of the output.
+template <int D, bool BF16, bool OUT_F32>
+__device__ __forceinline__ void pd_write_mix(const PdParams& p, size_t idx, int c4, PdMix x) {
+  const bool none = x.top == -INFINITY;
+  const float inv = none ? 0.f : 1.f / x.tot;
+  x.r.x *= inv;
+  x.r.y *= inv;
+  x.r.z *= inv;
+  x.r.w *= inv;
   if constexpr (OUT_F32) {
-    reinterpret_cast<float4*>(static_cast<float*>(p.o) + idx * D)[c4] = r;
+    reinterpret_cast<float4*>(static_cast<float*>(p.o) + idx * D)[c4] = x.r;
   } else {
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + idx * D)[c4] =
-        make_uint2(pack2<BF16>(r.x, r.y), pack2<BF16>(r.z, r.w));
+        make_uint2(pack2<BF16>(x.r.x, x.r.y), pack2<BF16>(x.r.z, x.r.w));
   }
-  if (c4 == 0 && p.lse != nullptr) p.lse[idx] = none ? -INFINITY : mx + logf(tot);
+  if (c4 == 0 && p.lse != nullptr) p.lse[idx] = none ? -INFINITY : x.top + logf(x.tot);
+}
+
+// The rows of sequence b, which keeps nothing: zeros and minus infinity.
+template <int D, bool OUT_F32>
+__device__ __forceinline__ void pd_write_empty(const PdParams& p, int b) {
+  const size_t row0 = static_cast<size_t>(b) * p.H * p.N_q;
+  const int rows = p.H * p.N_q;
+  constexpr int VEC = D * (OUT_F32 ? 4 : 2) / 16;
+  uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) + row0 * D * (OUT_F32 ? 4 : 2));
+  for (int i = threadIdx.x; i < rows * VEC; i += PD_THREADS) o[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (p.lse != nullptr)
+    for (int i = threadIdx.x; i < rows; i += PD_THREADS) p.lse[row0 + i] = -INFINITY;
 }
 
 // Without a shared prefix: CTA c takes the group that the boundary behind
@@ -929,7 +996,7 @@ __global__ void __launch_bounds__(PD_THREADS)
 attn_paged_merge(const PdParams p) {
   __shared__ int part[PD_WARPS + 2];
   const int HR = p.H_kv * p.row_tiles;
-  const PdSum sum = pd_sum(p, part, nullptr);
+  const PdSum sum = pd_sum<PD_THREADS>(p, part, nullptr);
   const PdCut cut = pd_cut(sum.total * HR, p.ranges);
   const int c = blockIdx.x;
   PdWalk w;
@@ -938,7 +1005,7 @@ attn_paged_merge(const PdParams p) {
   if (any) {
     w.x = pd_start(cut, c + 1) - 1;
     w.end = w.x + 1;
-    pd_locate(p, sum, w.x / HR, part, w.b, w.base);
+    pd_locate<PD_THREADS>(p, sum, w.x / HR, part, w.b, w.base);
     w.base *= HR;
     w.s = pd_seq(p, pd_len_of(p, w.b));
     pd_run_here(p, w);
@@ -949,49 +1016,79 @@ attn_paged_merge(const PdParams p) {
   }
   grid_dependency_wait();
   grid_launch_dependents();
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+    if (pd_len_of(p, b) == 0) pd_write_empty<D, OUT_F32>(p, b);
   if (!any) return;
   const int r_first = w.rt * p.m, n_rows = min(p.m, p.R - r_first);
   const size_t idx0 = (static_cast<size_t>(w.b) * p.H + w.h * p.G) * p.N_q + r_first;
-  for (int x = (c - c_first) * PD_THREADS + threadIdx.x; x < n_rows * (D / 4); x += cuts * PD_THREADS) {
-    const int r = x / (D / 4), c4 = x % (D / 4);
-    PdParts none;
-    none.n = 0;
-    pd_merge_row<D, BF16, OUT_F32>(p, idx0 + r, c4, pd_parts(p, cut, g_start, w.s.tiles, 0, r), none);
+  PdParts none;
+  none.n = 0;
+  // D / 4 threads a row.  Few rows of many parts: the CTA's SETS sets of
+  // threads share a row's parts; else each takes rows of its own.
+  constexpr int SETS = PD_THREADS / (D / 4);
+  const int set = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
+  const int mine = c - c_first;
+  if (cuts + 1 > 8 && n_rows <= 2 * cuts) {
+    __shared__ PdMix mix[PD_THREADS];
+    for (int r = mine; r < n_rows; r += cuts) {
+      PdMix x = pd_mix<D>(c4, pd_parts(p, cut, g_start, w.s.tiles, 0, r), none, set, SETS);
+      mix[threadIdx.x] = x;
+      __syncthreads();
+      if (set == 0) {
+#pragma unroll
+        for (int v = 1; v < SETS; ++v) pd_join(x, mix[v * (D / 4) + c4]);
+        pd_write_mix<D, BF16, OUT_F32>(p, idx0 + r, c4, x);
+      }
+      __syncthreads();
+    }
+  } else {
+    for (int r = mine * SETS + set; r < n_rows; r += cuts * SETS)
+      pd_write_mix<D, BF16, OUT_F32>(
+          p, idx0 + r, c4, pd_mix<D>(c4, pd_parts(p, cut, g_start, w.s.tiles, 0, r), none, 0, 1));
   }
 }
 
-// Behind a shared prefix: one CTA for each sequence, K/V head and row tile.
+// Behind a shared prefix every row has parts of the prefix and of its own
+// positions: D / 4 threads a row, rows in the order of the output.
 template <int D, bool BF16, bool OUT_F32>
 __global__ void __launch_bounds__(PD_THREADS)
 attn_paged_merge_shared(const PdParams p, const PdParams pre) {
   __shared__ int part[PD_WARPS + 2];
+  constexpr int SETS = PD_THREADS / (D / 4);
   const int HR = p.H_kv * p.row_tiles;
-  const int g = static_cast<int>(blockIdx.x % HR), b = static_cast<int>(blockIdx.x / HR);
+  const int rows_b = p.H * p.N_q, rows = p.B * rows_b;
+  const int row0 = static_cast<int>(static_cast<long long>(rows) * blockIdx.x / gridDim.x);
+  const int row1 = static_cast<int>(static_cast<long long>(rows) * (blockIdx.x + 1) / gridDim.x);
+  const int b0 = row0 / rows_b;
   int x = 0, all = 0, before, total;
   for (int i = threadIdx.x; i < p.B; i += PD_THREADS) {
     const int tiles = pd_seq(p, pd_len_of(p, i)).tiles;
     all += tiles;
-    if (i < b) x += tiles;
+    if (i < b0) x += tiles;
   }
-  pd_scan(x, part, before);
-  pd_scan(all, part, total);
+  pd_scan<PD_THREADS>(x, part, before);
+  pd_scan<PD_THREADS>(all, part, total);
   const PdCut cut = pd_cut(total * HR, p.ranges);
   const PdCut p_cut = pd_cut(pre.shared_tiles * pre.H_kv * pre.row_tiles, pre.ranges);
-  const PdSeq s = pd_seq(p, pd_len_of(p, b));
-  const int g_start = before * HR + g * s.tiles;
-  const int h = g / p.row_tiles, r_first = (g - h * p.row_tiles) * p.m;
-  const int n_rows = min(p.m, p.R - r_first);
-  const size_t group = static_cast<size_t>(b) * HR + g;
-  const size_t idx0 = (static_cast<size_t>(b) * p.H + h * p.G) * p.N_q + r_first;
+  int b = b0;
+  PdSeq s = pd_seq(p, pd_len_of(p, b));
+  const int set = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int i = threadIdx.x; i < n_rows * (D / 4); i += PD_THREADS) {
-    const int r = i / (D / 4), c4 = i % (D / 4);
-    const int pr = b * p.R + r_first + r;         // row of the prefix
+  for (int row = row0 + set; row < row1; row += SETS) {
+    for (; row >= (b + 1) * rows_b; s = pd_seq(p, pd_len_of(p, b))) {
+      before += s.tiles;
+      ++b;
+    }
+    int r = row - b * rows_b;
+    const int h = r / p.R;
+    r -= h * p.R;                                 // of the R rows of (b, h)
+    const int g = h * p.row_tiles + r / p.m;
+    const int pr = b * p.R + r;                   // row of the prefix
     const int pg = h * pre.row_tiles + pr / pre.m;
-    pd_merge_row<D, BF16, OUT_F32>(p, idx0 + r, c4,
-                                   pd_parts(pre, p_cut, pg * pre.shared_tiles, pre.shared_tiles, pg, pr % pre.m),
-                                   pd_parts(p, cut, g_start, s.tiles, group, r));
+    const PdParts a = pd_parts(pre, p_cut, pg * pre.shared_tiles, pre.shared_tiles, pg, pr % pre.m);
+    const PdParts own = pd_parts(p, cut, before * HR + g * s.tiles, s.tiles, static_cast<size_t>(b) * HR + g, r % p.m);
+    pd_write_mix<D, BF16, OUT_F32>(p, row, c4, pd_mix<D>(c4, a, own, 0, 1));
   }
 }
 

@@ -153,7 +153,7 @@ def test_workspace_queries():
     assert need(-1, 4, 2, 1, 64) == -1 and need(3, 5, 2, 1, 64) == -1 and need(3, 4, 0, 1, 64) == -1
     assert need(3, 4, 2, 1, 64, -1) == -1
     assert 0 < need(3, 4, 2, 1, 64) < need(3, 4, 2, 1, 128) < 16 << 20
-    assert need(3, 4, 2, 1, 64, 15) == need(3, 4, 2, 1, 64) < need(3, 4, 2, 1, 64, 128)
+    assert need(3, 4, 2, 1, 64, 127) == need(3, 4, 2, 1, 64) < need(3, 4, 2, 1, 64, 128)
     lib = A.load_library()
     assert lib.attn_pages_append_workspace_bytes(-1, 1, 16) == -1
     assert lib.attn_pages_append_workspace_bytes(4, 100, 16) >= 4 * (6 * 4 + 4 * 8)
