@@ -158,12 +158,12 @@ int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams
   if (rc != ATTN_OK) return rc;
   if (pre != nullptr) {
     // a CTA for as many rows as it takes at once, four CTAs on an SM at most
-    const int at_once = attn::PD_THREADS / (D / 4), rows = dp.B * dp.H * dp.N_q;
+    const int at_once = attn::PD_MERGE / (D / 4), rows = dp.B * dp.H * dp.N_q;
     const int grid = (rows + at_once - 1) / at_once;
     return counted(launch_overlapped(attn::attn_paged_merge_shared<D, BF16, F32>, grid < 592 ? grid : 592,
-                                     attn::PD_THREADS, 0, stream, dp, *pre));
+                                     attn::PD_MERGE, 0, stream, dp, *pre));
   }
-  return counted(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges, attn::PD_THREADS, 0, stream, dp));
+  return counted(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges, attn::PD_MERGE, 0, stream, dp));
 }
 
 }  // namespace

@@ -28,9 +28,10 @@
 namespace attn {
 
 constexpr int PD_TILE = 64;             // positions of a tile
-constexpr int PD_SLICE = 16;            // positions a warp loads and attends at a time
+constexpr int PD_SLICE = 16;            // positions of a tile that a warp attends
 constexpr int PD_WARPS = PD_TILE / PD_SLICE;
-constexpr int PD_THREADS = 32 * PD_WARPS;
+constexpr int PD_THREADS = 32 * (PD_WARPS + 1);   // and a warp that loads
+constexpr int PD_MERGE = 128;           // threads of the merging kernels
 constexpr int PD_LENS = 512;            // lengths kept in shared memory
 
 struct PdParams {
@@ -61,8 +62,9 @@ struct PdParams {
 };
 
 // Shared memory of head dimension D and 8 NT rows a group: a ring of NST
-// slices (K, then V) for each warp, the exchange buffer of the epilogue, row
-// statistics, a run's query rows, the first sequences' lengths, barriers.
+// tiles (the slices of K, then those of V), a run's query rows, the exchange
+// buffer of the epilogue, row statistics, the first sequences' lengths,
+// barriers.
 template <int D, int NT>
 struct PdGeo {
   static_assert(D == 64 || D == 128, "the paged decoding kernel supports d = 64 and 128");
@@ -70,20 +72,20 @@ struct PdGeo {
   static constexpr int NST = D == 128 ? 3 : 6;
   static constexpr int NCH = D / 64;                    // 64-column chunks, 128-byte swizzle
   static constexpr int CHUNK_BYTES = PD_SLICE * 128;
-  static constexpr int HALF_BYTES = NCH * CHUNK_BYTES;  // K (or V) of a slice
+  static constexpr int SLICE_BYTES = NCH * CHUNK_BYTES; // K (or V) of a slice
+  static constexpr int HALF_BYTES = PD_WARPS * SLICE_BYTES;
   static constexpr int STAGE_BYTES = 2 * HALF_BYTES;
-  static constexpr int RING_BYTES = PD_WARPS * NST * STAGE_BYTES;
-  static constexpr int Q_CHUNK = M * 128;               // the query rows in the same chunks
+  static constexpr int RING_BYTES = NST * STAGE_BYTES;
+  static constexpr int Q_LD = D * 2 + 16;               // bytes from row to row: no bank conflicts
   static constexpr int Q_OFF = RING_BYTES;
-  static constexpr int Q_VECS = M * D / 8;              // 16-byte vectors of the rows
   static constexpr int X_ROWS = 512 / D;                // rows combined at a time
   static constexpr int X_LD = D + 4;                    // floats from row to row
-  static constexpr int X_OFF = Q_OFF + NCH * Q_CHUNK;   // float [PD_WARPS][X_ROWS][X_LD]
+  static constexpr int X_OFF = Q_OFF + M * Q_LD;        // float [PD_WARPS][X_ROWS][X_LD]
   static constexpr int STAT_OFF = X_OFF + PD_WARPS * X_ROWS * X_LD * 4;   // float [3][PD_WARPS][M]
   static constexpr int LENS_OFF = STAT_OFF + 3 * PD_WARPS * M * 4;
-  static constexpr int BAR_OFF = LENS_OFF + PD_LENS * 4;
-  static constexpr int SCAN_OFF = BAR_OFF + PD_WARPS * NST * 8;   // int [PD_WARPS + 2]
-  static constexpr int ABORT_OFF = SCAN_OFF + (PD_WARPS + 2) * 4;
+  static constexpr int BAR_OFF = LENS_OFF + PD_LENS * 4;   // full [NST], empty [NST], rows full, rows empty
+  static constexpr int SCAN_OFF = BAR_OFF + (2 * NST + 2) * 8;   // int [PD_THREADS / 32 + 2]
+  static constexpr int ABORT_OFF = SCAN_OFF + (PD_THREADS / 32 + 2) * 4;
   static constexpr int SMEM_BYTES = ABORT_OFF + 8;
   // two CTAs on an SM
   static_assert(2 * (SMEM_BYTES + 2048) <= 233472, "shared memory budget");
@@ -130,11 +132,10 @@ __device__ __forceinline__ PdSeq pd_seq(const PdParams& p, int len) {
   return s;
 }
 
-// Lengths that do not fit the table are reported once.
-template <int THREADS>
+// Lengths that do not fit the table are reported once, by one warp.
 __device__ __forceinline__ void pd_report_lens(const PdParams& p) {
   if (blockIdx.x != 0) return;
-  for (int b = threadIdx.x; b < p.B; b += THREADS) {
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
     const int n = p.lens[b];
     if (n < 0 || n > (p.max_pages << p.page_shift)) atomicCAS(p.status, 0, -1);
   }
@@ -305,12 +306,6 @@ __device__ __forceinline__ int pd_key(const PdSeq& s, int i, int warp) {
   return (i < s.sb ? i : s.w0 + (i - s.sb)) * PD_TILE + warp * PD_SLICE;
 }
 
-// The run's tiles [i0, pd_stop) hold positions of the warp's slice.
-__device__ __forceinline__ int pd_stop(const PdWalk& w, int warp) {
-  const int t = max(0, w.s.len - warp * PD_SLICE + PD_TILE - 1) / PD_TILE;
-  return min(w.i_end, t > w.s.w0 ? w.s.sb + t - w.s.w0 : min(w.s.sb, t));
-}
-
 // Under a window, whether no row of the sequence keeps one of the n positions
 // from key0 on: they are neither loaded nor looked up in the table.
 __device__ __forceinline__ bool pd_gone(const PdParams& p, const PdSeq& s, int key0, int n = PD_SLICE) {
@@ -327,10 +322,6 @@ __device__ __forceinline__ void pd_ldsm(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void pd_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-
-__device__ __forceinline__ void prefetch_l2(const void* a) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit values, two of a row a lane.
@@ -387,18 +378,136 @@ __device__ __forceinline__ void pd_row_keeps(const PdParams& p, const PdWalk& w,
   lo = p.window > 0 ? pos - p.window + 1 : 0;
 }
 
+// ------------------------------------------------------------ loading warp
+
+// Rows of q into shared memory: untiled copies, 16-byte aligned and a
+// multiple of 16 bytes long.
+__device__ __forceinline__ void pd_copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void pd_sync_attending() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * PD_WARPS) : "memory");
+}
+
+// Up to PD_BATCH tiles of a run, and in lane 4 j + s the page of slice s of
+// its j-th tile (-1: the slice is not loaded; n_pages: the entry is bad, so the
+// box lies outside the tensor and is filled with zeros).
+constexpr int PD_BATCH = 32 / PD_WARPS;
+
+struct PdBatch {
+  PdWalk w;
+  int i, n;
+  int page;
+};
+
+__device__ __forceinline__ void pd_look_up(const PdParams& p, PdBatch& t, int lane) {
+  t.n = min(PD_BATCH, t.w.i_end - t.i);
+  t.page = -1;
+  const int j = lane / PD_WARPS;
+  if (j < t.n) {
+    const int key = pd_key(t.w.s, t.i + j, lane % PD_WARPS);
+    if (key < t.w.s.len && !pd_gone(p, t.w.s, key)) {
+      const int page = p.table[(p.prefix ? 0 : static_cast<size_t>(t.w.b) * p.max_pages) + (key >> p.page_shift)];
+      t.page = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages) ? page : p.n_pages;
+    }
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void pd_load_role(const PdParams& p, const PdWalk& w0, const CUtensorMap* tmK,
+                                          const CUtensorMap* tmV, uint32_t ring, uint32_t q_tile, uint32_t full,
+                                          uint32_t empty, uint32_t q_full, uint32_t q_empty, const int* lens_s,
+                                          int lane, volatile int* abort_flag) {
+  using T = PdGeo<D, NT>;
+  uint32_t stage = 0, phase = 1, q_phase = 1;           // parities of the empty barriers
+  uint32_t issued = 0, q_issued = 0;
+  bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    const bool x = mbar_try_wait(bar, par) || wait_slow(bar, par, abort_flag, p.status, p.watchdog_ns);
+    return __all_sync(0xffffffffu, x);
+  };
+  // one batch is loaded while the next one's pages are looked up
+  PdBatch t, next;
+  t.w = w0;
+  t.i = w0.i0;
+  pd_look_up(p, t, lane);
+  bool fresh = true;                                    // t begins a run
+  for (bool more = true; more && ok;) {
+    next = t;
+    next.i += t.n;
+    const bool next_run = next.i >= next.w.i_end;
+    if (next_run) {
+      more = pd_next_run(p, next.w, lens_s);
+      next.i = next.w.i0;
+    }
+    if (more) pd_look_up(p, next, lane);
+    if (fresh) {
+      ok = wait(q_empty, q_phase);
+      if (!ok) break;
+      q_phase ^= 1u;
+      const int rows = pd_rows(p, t.w);
+      if (elect_one()) mbar_arrive_expect_tx(q_full, rows * D * 2);
+      __syncwarp();
+      if (lane < rows)
+        pd_copy_row(q_tile + lane * T::Q_LD, static_cast<const uint16_t*>(p.q) + pd_row_index(p, t.w, lane) * D, D * 2,
+                    q_full);
+      __syncwarp();
+      ++q_issued;
+    }
+    for (int j = 0; j < t.n; ++j) {
+      const uint32_t have = __ballot_sync(0xffffffffu, t.page >= 0) >> (j * PD_WARPS) & ((1u << PD_WARPS) - 1);
+      ok = wait(empty + 8 * stage, phase);
+      if (!ok) break;
+      const uint32_t bar = full + 8 * stage, dst = ring + stage * T::STAGE_BYTES;
+      const int y0 = pd_tile_key(p, t.w.s, t.i + j) & ((1 << p.page_shift) - 1);
+      if (elect_one()) mbar_arrive_expect_tx(bar, __popc(have) * 2 * T::SLICE_BYTES);
+      __syncwarp();
+#pragma unroll
+      for (int s = 0; s < PD_WARPS; ++s) {
+        const int page = __shfl_sync(0xffffffffu, t.page, j * PD_WARPS + s);
+        if (page < 0) continue;
+        const int z = page < p.n_pages ? page * p.H_kv + t.w.h : -1;
+        const int y = (y0 + s * PD_SLICE) & ((1 << p.page_shift) - 1);
+        if (elect_one()) {
+          if (z < 0) atomicCAS(p.status, 0, -1);
+          tma_load_4d(dst + s * T::SLICE_BYTES, tmK, bar, 0, y, 0, z);
+          tma_load_4d(dst + T::HALF_BYTES + s * T::SLICE_BYTES, tmV, bar, 0, y, 0, z);
+        }
+        __syncwarp();
+      }
+      ++issued;
+      if (++stage == T::NST) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    t = next;
+    fresh = next_run;
+  }
+  // after an expired wait, the copies still in flight
+  if (!ok) {
+    for (uint32_t i = issued > T::NST ? issued - T::NST : 0; i < issued; ++i)
+      drain_wait(full + 8 * (i % T::NST), (i / T::NST) & 1u, p.watchdog_ns);
+    if (q_issued > 0) drain_wait(q_full, (q_issued - 1) & 1u, p.watchdog_ns);
+  }
+}
+
 // ------------------------------------------------------------ attending kernel
 
-// Each warp streams its own slices: slice `warp` of every tile of the range,
-// through its own ring of TMA loads, with its own running (m, l, O) for the
-// group's rows in registers.  No warp waits for another before the end of a
-// run, where the warps' results are combined through shared memory; the next
-// runs' slices are in flight meanwhile.
+// PD_WARPS warps attend and one loads.  The loading warp looks up pages and
+// brings tiles (and each run's query rows) through a ring of TMA loads, runs
+// ahead of the others.  An attending warp takes slice `warp` of every tile of
+// the range, with its own running (m, l, O) for the group's rows in registers;
+// none waits for another before the end of a run, where their results are
+// combined through shared memory.
 //
-// Bound: HBM.  A slice is 16 rows of K and of V; two CTAs' rings keep 192 KB
-// a SM in flight.  With two warps on each scheduler the instructions of a
-// slice bound the rate next, so they are kept few.  The products are taken
-// transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync 16 x 8 x 16, 16
+// Bound: HBM.  Two CTAs' rings keep 192 KB a SM in flight.  With two attending
+// warps on each scheduler the instructions of a slice bound the rate next,
+// so they are kept few: the integer work of the loads is the loading warp's (in the
+// attending warps it took half of a slice's 1300 cycles), and the products are
+// taken transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync 16 x 8 x 16, 16
 // positions or 16 columns by 8 query rows), so that up to 8 rows, the query heads
 // of a K/V head at one new row each, cost half of what a 16-row tile of Q would;
 // tcgen05's 128 rows would cost 16 times that and as many more exponentials.
@@ -415,18 +524,23 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   int* lens_s = reinterpret_cast<int*>(smem + T::LENS_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::ABORT_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t ring = smem_addr(smem) + warp * T::NST * T::STAGE_BYTES;
-  const uint32_t bars = smem_addr(smem) + T::BAR_OFF + warp * T::NST * 8;
+  const uint32_t ring = smem_addr(smem);
+  const uint32_t full = smem_addr(smem) + T::BAR_OFF, empty = full + 8 * T::NST;
+  const uint32_t q_full = empty + 8 * T::NST, q_empty = q_full + 8;
+  const uint32_t q_tile = smem_addr(smem) + T::Q_OFF;
   float* xbuf = reinterpret_cast<float*>(smem + T::X_OFF);
   float* stat = reinterpret_cast<float*>(smem + T::STAT_OFF);
-  if (lane == 0) {
-    for (int s = 0; s < T::NST; ++s) mbar_init(bars + 8 * s, 1);
-    fence_barrier_init();
-    if (warp == 0) {
-      *abort_flag = 0;
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::NST; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, PD_WARPS);
     }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, PD_WARPS);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   grid_dependency_wait();
   grid_launch_dependents();
@@ -435,7 +549,10 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const int HR = p.H_kv * p.row_tiles;
   const PdSum sum = pd_sum<PD_THREADS>(p, part, lens_s);
   const PdCut cut = pd_cut(sum.total * HR, gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= cut.n) return;
+  if (static_cast<int>(blockIdx.x) >= cut.n) {
+    if (warp == PD_WARPS) pd_report_lens(p);
+    return;
+  }
   PdWalk w;
   const int f0 = pd_start(cut, blockIdx.x);
   w.x = f0;
@@ -445,93 +562,12 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   w.s = pd_seq(p, pd_len_of(p, w.b, lens_s));
   pd_run_here(p, w);
 
-  // ---- this warp's loads: the slice to load next.  Lane l looks up the page of
-  // this warp's slice of tile l_base + l, 32 tiles at a time.
-  PdWalk lw = w;
-  int li = lw.i0 - 1, l_stop = pd_stop(lw, warp), l_base = -32, l_pages = 0;
-  bool l_more = true;
-  uint32_t l_stage = 0;
-  uint32_t loaded = 0;
-  auto advance = [&]() {
-    for (;;) {
-      if (++li >= l_stop) {
-        l_more = pd_next_run(p, lw, lens_s);
-        if (!l_more) return;
-        l_stop = pd_stop(lw, warp);
-        li = -1;
-        l_base = -32;
-        if (warp == 0 && lane < pd_rows(p, lw))
-          prefetch_l2(static_cast<const uint16_t*>(p.q) + pd_row_index(p, lw, lane) * D);
-        continue;
-      }
-      if (li >= l_base + 32 || l_base < 0) {
-        l_base = li;
-        l_pages = -1;
-        const int key = pd_key(lw.s, li + lane, warp);
-        if (li + lane < l_stop && !pd_gone(p, lw.s, key))
-          l_pages = p.table[(p.prefix ? 0 : static_cast<size_t>(lw.b) * p.max_pages) + (key >> p.page_shift)];
-      }
-      if (!pd_gone(p, lw.s, pd_key(lw.s, li, warp))) break;
-    }
-  };
-  auto refill = [&]() {
-    if (!l_more) return;
-    const int l_page = __shfl_sync(0xffffffffu, l_pages, li - l_base);
-    if (elect_one()) {
-      const uint32_t bar = bars + 8 * l_stage;
-      const uint32_t dst = ring + l_stage * T::STAGE_BYTES;
-      const bool good = static_cast<unsigned>(l_page) < static_cast<unsigned>(p.n_pages);
-      // a bad page's box lies outside the tensor and is filled with zeros
-      const int z = good ? l_page * p.H_kv + lw.h : -1;
-      const int y = pd_key(lw.s, li, warp) & ((1 << p.page_shift) - 1);
-      if (!good) atomicCAS(p.status, 0, -1);
-      if (!p.withhold_loads) {
-        mbar_arrive_expect_tx(bar, T::STAGE_BYTES);
-        tma_load_4d(dst, &tmK, bar, 0, y, 0, z);
-        tma_load_4d(dst + T::HALF_BYTES, &tmV, bar, 0, y, 0, z);
-      }
-    }
-    __syncwarp();
-    ++loaded;
-    if (++l_stage == T::NST) l_stage = 0;
-    advance();
-  };
-
-  // ---- a run's rows.  They go through shared memory (fetch, store), from
-  // where every warp takes the B operands.
-  const uint32_t q_tile = smem_addr(smem) + T::Q_OFF;
-  struct QPart {
-    uint4 x[(T::Q_VECS + PD_THREADS - 1) / PD_THREADS];
-  };
-  auto fetch_q = [&]() {
-    QPart f;
-    const int n = pd_rows(p, w);
-#pragma unroll
-    for (int u = 0; u * PD_THREADS < T::Q_VECS; ++u) {
-      const int r = (threadIdx.x + u * PD_THREADS) / (D / 8), c = (threadIdx.x + u * PD_THREADS) % (D / 8);
-      f.x[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < n)
-        f.x[u] = *(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + pd_row_index(p, w, r) * D) + c);
-    }
-    return f;
-  };
-  auto store_q = [&](const QPart& f) {
-#pragma unroll
-    for (int u = 0; u * PD_THREADS < T::Q_VECS; ++u) {
-      const int r = (threadIdx.x + u * PD_THREADS) / (D / 8), c = (threadIdx.x + u * PD_THREADS) % (D / 8);
-      if (r < M)
-        st_shared_v4(q_tile + (c >> 3) * T::Q_CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4), f.x[u].x, f.x[u].y,
-                     f.x[u].z, f.x[u].w);
-    }
-  };
-  {
-    const QPart x = fetch_q();
-    advance();
-    for (int s = 0; s < T::NST; ++s) refill();
-    store_q(x);
+  if (warp == PD_WARPS) {
+    if (!p.withhold_loads)   // failure-detection test: every wait on a tile runs out
+      pd_load_role<D, NT>(p, w, &tmK, &tmV, ring, q_tile, full, empty, q_full, q_empty, lens_s, lane, abort_flag);
+    pd_report_lens(p);
+    return;
   }
-  pd_report_lens<PD_THREADS>(p);
-  __syncthreads();
 
   // Fragments: lane 4 g + t holds positions g and g + 8 (of K's slice) or
   // columns g and g + 8 (of V's 16), and query rows 8 n + 2 t and 8 n + 2 t + 1.
@@ -554,23 +590,35 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
   constexpr uint32_t one2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
   const uint32_t ones[4] = {one2, one2, one2, one2};
-  uint32_t done = 0, waited = 0;   // slices passed; slices whose loads have landed
-  uint32_t stage = 0, phase = 0;
+  uint32_t stage = 0, phase = 0, q_phase = 0;
   bool ok = true;
+  // Whether the barrier's phase is over; after an expired wait the warp goes on
+  // to the end without waiting, so that no barrier of the CTA is missed.
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    if (ok) {
+      ok = mbar_try_wait(bar, par) || wait_slow(bar, par, abort_flag, p.status, p.watchdog_ns);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    return ok;
+  };
 
   for (bool more = true; more;) {
     uint32_t qf[D / 16][NT][2];
+    wait(q_full, q_phase);
+    q_phase ^= 1u;
 #pragma unroll
     for (int k = 0; k < D / 32; ++k)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t x[4];
-        pd_ldsm(q_tile + (k >> 1) * T::Q_CHUNK + (n * 8 + mr) * 128 + ((((k & 1) * 4 + mat) ^ mr) << 4), x);
+        pd_ldsm(q_tile + (n * 8 + mr) * T::Q_LD + (4 * k + mat) * 16, x);
         qf[2 * k][n][0] = x[0] ^ q_sign;
         qf[2 * k][n][1] = x[1] ^ q_sign;
         qf[2 * k + 1][n][0] = x[2] ^ q_sign;
         qf[2 * k + 1][n][1] = x[3] ^ q_sign;
       }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty);
     // limits of this lane's rows, and the positions that some row keeps and
     // that all rows keep
     int hi[NT][2], lo[NT][2];
@@ -613,23 +661,20 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       le[n][0] = le[n][1] = 0.f;
     }
 
-    const int i_stop = pd_stop(w, warp);
-    for (int i = w.i0; i < i_stop; ++i) {
+    for (int i = w.i0; i < w.i_end; ++i) {
       const int key0 = pd_key(w.s, i, warp);
-      if (pd_gone(p, w.s, key0)) continue;
-      const uint32_t ks = ring + stage * T::STAGE_BYTES, vs = ks + T::HALF_BYTES;
-      if (ok) {
-        const uint32_t bar = bars + 8 * stage;
-        ok = mbar_try_wait(bar, phase) || wait_slow(bar, phase, abort_flag, p.status, p.watchdog_ns);
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      ++done;
+      const uint32_t ks = ring + stage * T::STAGE_BYTES + warp * T::SLICE_BYTES, vs = ks + T::HALF_BYTES;
+      const uint32_t free_bar = empty + 8 * stage;
+      wait(full + 8 * stage, phase);
       if (++stage == T::NST) {
         stage = 0;
         phase ^= 1u;
       }
-      if (!ok) continue;
-      waited = done;
+      // a slice with no position that a row may keep was not loaded
+      if (!ok || key0 >= w.s.len || pd_gone(p, w.s, key0)) {
+        if (lane == 0) mbar_arrive(free_bar);
+        continue;
+      }
       // S^T, the even and the odd steps of d summed apart (two chains)
       float s[NT][4] = {}, s2[NT][4] = {};
 #pragma unroll
@@ -729,8 +774,8 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           for (int n = 0; n < NT; ++n) pd_mma<BF16>(acc[k][n], vf, pf[n][0], pf[n][1]);
         }
       }
-      __syncwarp();   // every lane has read the stage
-      refill();
+      __syncwarp();   // every lane has read the slice
+      if (lane == 0) mbar_arrive(free_bar);
     }
 
     // ---- the run's result: the warps' (m, l, O) combined
@@ -764,10 +809,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       row = (2 * static_cast<size_t>(blockIdx.x) + (w.x == f0 ? 0 : 1)) * M;
     else
       row = (static_cast<size_t>(w.b) * HR + w.h * p.row_tiles + w.rt) * M;
-    // the next run's rows are on their way while this one is finished
     more = pd_next_run(p, w, lens_s);
-    QPart q_next;
-    if (more) q_next = fetch_q();
 
     constexpr int XR = T::X_ROWS;
 #pragma unroll
@@ -786,8 +828,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           xw[16 * k + 8 + T::X_LD] = a[3];
         }
       }
-      __syncthreads();
-      if (more && r0 + XR >= n_rows) store_q(q_next);   // every warp has its B operands
+      pd_sync_attending();
       // this thread: four columns of one row
       const int xr = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4), r = r0 + xr;
       if (r < n_rows) {
@@ -827,13 +868,8 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           else if (p.lse != nullptr) p.lse[row + r] = z;
         }
       }
-      __syncthreads();
+      pd_sync_attending();
     }
-  }
-  // after an expired wait, the copies still in flight
-  if (!ok && !p.withhold_loads) {
-    for (; waited < loaded; ++waited)
-      drain_wait(bars + 8 * (waited % T::NST), (waited / T::NST) & 1u, p.watchdog_ns);
   }
 }
 
@@ -979,9 +1015,9 @@ __device__ __forceinline__ void pd_write_empty(const PdParams& p, int b) {
   const int rows = p.H * p.N_q;
   constexpr int VEC = D * (OUT_F32 ? 4 : 2) / 16;
   uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) + row0 * D * (OUT_F32 ? 4 : 2));
-  for (int i = threadIdx.x; i < rows * VEC; i += PD_THREADS) o[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = threadIdx.x; i < rows * VEC; i += PD_MERGE) o[i] = make_uint4(0u, 0u, 0u, 0u);
   if (p.lse != nullptr)
-    for (int i = threadIdx.x; i < rows; i += PD_THREADS) p.lse[row0 + i] = -INFINITY;
+    for (int i = threadIdx.x; i < rows; i += PD_MERGE) p.lse[row0 + i] = -INFINITY;
 }
 
 // Without a shared prefix: CTA c takes the group that the boundary behind
@@ -992,11 +1028,11 @@ __device__ __forceinline__ void pd_write_empty(const PdParams& p, int b) {
 // CTA of the attending kernel had passed its own when this one was launched,
 // so what ran before that kernel is complete, and it writes no lengths.
 template <int D, bool BF16, bool OUT_F32>
-__global__ void __launch_bounds__(PD_THREADS)
+__global__ void __launch_bounds__(PD_MERGE)
 attn_paged_merge(const PdParams p) {
-  __shared__ int part[PD_WARPS + 2];
+  __shared__ int part[PD_MERGE / 32 + 2];
   const int HR = p.H_kv * p.row_tiles;
-  const PdSum sum = pd_sum<PD_THREADS>(p, part, nullptr);
+  const PdSum sum = pd_sum<PD_MERGE>(p, part, nullptr);
   const PdCut cut = pd_cut(sum.total * HR, p.ranges);
   const int c = blockIdx.x;
   PdWalk w;
@@ -1005,7 +1041,7 @@ attn_paged_merge(const PdParams p) {
   if (any) {
     w.x = pd_start(cut, c + 1) - 1;
     w.end = w.x + 1;
-    pd_locate<PD_THREADS>(p, sum, w.x / HR, part, w.b, w.base);
+    pd_locate<PD_MERGE>(p, sum, w.x / HR, part, w.b, w.base);
     w.base *= HR;
     w.s = pd_seq(p, pd_len_of(p, w.b));
     pd_run_here(p, w);
@@ -1025,11 +1061,11 @@ attn_paged_merge(const PdParams p) {
   none.n = 0;
   // D / 4 threads a row.  Few rows of many parts: the CTA's SETS sets of
   // threads share a row's parts; else each takes rows of its own.
-  constexpr int SETS = PD_THREADS / (D / 4);
+  constexpr int SETS = PD_MERGE / (D / 4);
   const int set = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
   const int mine = c - c_first;
   if (cuts + 1 > 8 && n_rows <= 2 * cuts) {
-    __shared__ PdMix mix[PD_THREADS];
+    __shared__ PdMix mix[PD_MERGE];
     for (int r = mine; r < n_rows; r += cuts) {
       PdMix x = pd_mix<D>(c4, pd_parts(p, cut, g_start, w.s.tiles, 0, r), none, set, SETS);
       mix[threadIdx.x] = x;
@@ -1051,23 +1087,23 @@ attn_paged_merge(const PdParams p) {
 // Behind a shared prefix every row has parts of the prefix and of its own
 // positions: D / 4 threads a row, rows in the order of the output.
 template <int D, bool BF16, bool OUT_F32>
-__global__ void __launch_bounds__(PD_THREADS)
+__global__ void __launch_bounds__(PD_MERGE)
 attn_paged_merge_shared(const PdParams p, const PdParams pre) {
-  __shared__ int part[PD_WARPS + 2];
-  constexpr int SETS = PD_THREADS / (D / 4);
+  __shared__ int part[PD_MERGE / 32 + 2];
+  constexpr int SETS = PD_MERGE / (D / 4);
   const int HR = p.H_kv * p.row_tiles;
   const int rows_b = p.H * p.N_q, rows = p.B * rows_b;
   const int row0 = static_cast<int>(static_cast<long long>(rows) * blockIdx.x / gridDim.x);
   const int row1 = static_cast<int>(static_cast<long long>(rows) * (blockIdx.x + 1) / gridDim.x);
   const int b0 = row0 / rows_b;
   int x = 0, all = 0, before, total;
-  for (int i = threadIdx.x; i < p.B; i += PD_THREADS) {
+  for (int i = threadIdx.x; i < p.B; i += PD_MERGE) {
     const int tiles = pd_seq(p, pd_len_of(p, i)).tiles;
     all += tiles;
     if (i < b0) x += tiles;
   }
-  pd_scan<PD_THREADS>(x, part, before);
-  pd_scan<PD_THREADS>(all, part, total);
+  pd_scan<PD_MERGE>(x, part, before);
+  pd_scan<PD_MERGE>(all, part, total);
   const PdCut cut = pd_cut(total * HR, p.ranges);
   const PdCut p_cut = pd_cut(pre.shared_tiles * pre.H_kv * pre.row_tiles, pre.ranges);
   int b = b0;

@@ -540,7 +540,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     n = __reduce_max_sync(0xffffffffu, n);
     if (lane == 0) atomicMax(longest_s, n);
   }
-  pd_report_lens<NUM_THREADS>(p);
+  if (warp == NUM_THREADS / 32 - 1) pd_report_lens(p);
   const PdCut cut = pd_cut(sum.total * HR, gridDim.x);
   const bool any = static_cast<int>(blockIdx.x) < cut.n;
   PdWalk w;
