@@ -17,6 +17,7 @@ constexpr int kSharedUnit = 128;      // the shared prefix is attended in whole 
 // fixed, so that the workspace can be sized without a device.
 struct PagedForm {
   int m, row_tiles, tile_shift, ranges;
+  int weight;   // 100 cycles of an SM a tile
 };
 
 PagedForm paged_form(long long rows) {
@@ -25,6 +26,7 @@ PagedForm paged_form(long long rows) {
   f.row_tiles = static_cast<int>((rows + f.m - 1) / f.m);
   f.tile_shift = f.m <= 16 ? 6 : 7;
   f.ranges = f.m <= 16 ? 296 : 148;
+  f.weight = f.m <= 16 ? 7 : f.m == 128 ? 21 : 42;
   return f;
 }
 
@@ -84,14 +86,17 @@ int encode_pages(CUtensorMap* map, const void* base, bool bf16, int d, int page_
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// 3-D view [z][page_size][d] of the same; a box is as many rows of 64 columns
-// as a page and a tile of attn_paged_tc_kernel have in common.
+// 5-D view [z][page_size / 8][d / 64][8][64] of the same; a box is as many
+// groups of 8 rows as a page and a tile of attn_paged_tc_kernel have in common.
 int encode_boxes(CUtensorMap* map, const void* base, bool bf16, int d, int page_size, int z) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(z)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(page_size) * d * 2};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(page_size < attn::PT_TILE ? page_size : attn::PT_TILE), 1u};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
-  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  const cuuint64_t dims[5] = {64u, 8u, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(page_size / 8),
+                              static_cast<cuuint64_t>(z)};
+  const cuuint64_t strides[4] = {row, 128u, 8 * row, page_size * row};
+  const int rows = page_size < attn::PT_TILE ? page_size : attn::PT_TILE;
+  const cuuint32_t box[5] = {64u, 8u, static_cast<cuuint32_t>(d / 64), static_cast<cuuint32_t>(rows / 8), 1u};
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -163,7 +168,10 @@ int launch_paged(DeviceState* st, const attn::PdParams& dp, const attn::PdParams
     return counted(launch_overlapped(attn::attn_paged_merge_shared<D, BF16, F32>, grid < 592 ? grid : 592,
                                      attn::PD_MERGE, 0, stream, dp, *pre));
   }
-  return counted(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges, attn::PD_MERGE, 0, stream, dp));
+  // groups of many rows are merged by several CTAs a boundary
+  const int subs = dp.m <= 16 ? 1 : dp.m / 16;
+  return counted(launch_overlapped(attn::attn_paged_merge<D, BF16, F32>, dp.ranges * subs, attn::PD_MERGE, 0, stream,
+                                   dp, subs));
 }
 
 }  // namespace
@@ -257,6 +265,7 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
     x.row_tiles = f.row_tiles;
     x.tile_shift = f.tile_shift;
     x.ranges = f.ranges;
+    x.weight = f.weight;
     x.part_o = reinterpret_cast<float*>(ws + s.part_o);
     x.part_lse = reinterpret_cast<float*>(ws + s.part_lse);
     x.own_o = reinterpret_cast<float*>(ws + s.own_o);
@@ -274,6 +283,10 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
     place(pre, pl.prefix_form, pl.prefix);
     pre.shared_tiles = (units * kSharedUnit) >> pre.tile_shift;
     dp.shared_tiles = (units * kSharedUnit) >> dp.tile_shift;
+    pre.own_weight = dp.weight;
+    pre.own_groups = H_kv * dp.row_tiles;
+    pre.own_tile_shift = dp.tile_shift;
+    pre.own_shared_tiles = dp.shared_tiles;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const attn::PdParams* pp = shared ? &pre : nullptr;

@@ -58,6 +58,11 @@ struct PdParams {
   int shared_tiles;     // whole tiles of the shared prefix
   int prefix;           // this launch attends the shared prefix
   int ranges;           // CTAs of the attending kernel
+  int weight;           // time of a tile on one SM (see pd_prefix_ranges)
+  int own_weight;       // prefix: that of the sequences' own launch,
+  int own_groups;       //   its groups a sequence
+  int own_tile_shift;   //   and its tiles
+  int own_shared_tiles; //   in the prefix
   int withhold_loads;   // test hook: no slice is loaded, so every wait runs out
 };
 
@@ -163,6 +168,24 @@ __device__ __forceinline__ int pd_range_of(const PdCut& c, int f) {
   return f < t ? f / (c.each + 1) : c.more + (f - t) / c.each;
 }
 
+// The prefix is bound by the tensor cores and exponentials, the sequences' own
+// positions by HBM, so the two launches share the SMs: the prefix takes the
+// part of them that its work is of all (`own`: tiles of the other launch's
+// groups), the other launch's CTAs the rest.  Weights are cycles of an SM a
+// tile, in hundreds, measured at d = 128.  A prefix of few rows is bound by HBM
+// itself and takes all.
+__device__ __forceinline__ int pd_prefix_ranges(const PdParams& pre, int own) {
+  if (pre.m <= 16) return pre.ranges;
+  const long long a = static_cast<long long>(pre.shared_tiles) * pre.H_kv * pre.row_tiles * pre.weight;
+  const long long b = static_cast<long long>(own) * pre.own_weight;
+  return max(static_cast<int>(pre.ranges * a / (a + b)), pre.ranges / 4);
+}
+
+// Tiles of a sequence's own positions in the other launch.
+__device__ __forceinline__ int pd_own_tiles(const PdParams& pre, int len) {
+  return max(0, ((len + (1 << pre.own_tile_shift) - 1) >> pre.own_tile_shift) - pre.own_shared_tiles);
+}
+
 // The sum of x over the CTA's THREADS threads before this one, and of all.
 // `part` holds THREADS / 32 + 2 ints of shared memory.
 template <int THREADS>
@@ -194,6 +217,7 @@ __device__ __forceinline__ int pd_scan(int x, int* part, int& total) {
 struct PdSum {
   int total;
   int before, tiles;    // of sequence threadIdx.x
+  int ranges;           // ranges of the tile space
 };
 
 // Also keeps the first PD_LENS lengths in shared memory when `lens_s` is given.
@@ -203,16 +227,20 @@ __device__ __forceinline__ PdSum pd_sum(const PdParams& p, int* part, int* lens_
   s.total = p.shared_tiles;
   s.before = 0;
   s.tiles = 0;
-  int rest = 0;
+  s.ranges = p.ranges;
+  int rest = 0, own = 0;
   for (int b = threadIdx.x; b < p.B; b += THREADS) {
     const int len = pd_len_of(p, b);
     if (lens_s != nullptr && b < PD_LENS) lens_s[b] = len;
     const int tiles = pd_seq(p, len).tiles;
     if (b < THREADS) s.tiles = tiles;
     else rest += tiles;
+    if (p.prefix) own += pd_own_tiles(p, len);
   }
   if (p.prefix) {
-    __syncthreads();
+    int total;
+    pd_scan<THREADS>(own, part, total);
+    s.ranges = pd_prefix_ranges(p, total * p.own_groups);
     return s;
   }
   s.before = pd_scan<THREADS>(s.tiles, part, s.total);
@@ -411,6 +439,7 @@ __device__ __forceinline__ void pd_look_up(const PdParams& p, PdBatch& t, int la
     if (key < t.w.s.len && !pd_gone(p, t.w.s, key)) {
       const int page = p.table[(p.prefix ? 0 : static_cast<size_t>(t.w.b) * p.max_pages) + (key >> p.page_shift)];
       t.page = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages) ? page : p.n_pages;
+      if (t.page == p.n_pages) atomicCAS(p.status, 0, -1);
     }
   }
 }
@@ -462,21 +491,23 @@ __device__ __forceinline__ void pd_load_role(const PdParams& p, const PdWalk& w0
       if (!ok) break;
       const uint32_t bar = full + 8 * stage, dst = ring + stage * T::STAGE_BYTES;
       const int y0 = pd_tile_key(p, t.w.s, t.i + j) & ((1 << p.page_shift) - 1);
-      if (elect_one()) mbar_arrive_expect_tx(bar, __popc(have) * 2 * T::SLICE_BYTES);
-      __syncwarp();
+      int z[PD_WARPS];
 #pragma unroll
       for (int s = 0; s < PD_WARPS; ++s) {
         const int page = __shfl_sync(0xffffffffu, t.page, j * PD_WARPS + s);
-        if (page < 0) continue;
-        const int z = page < p.n_pages ? page * p.H_kv + t.w.h : -1;
-        const int y = (y0 + s * PD_SLICE) & ((1 << p.page_shift) - 1);
-        if (elect_one()) {
-          if (z < 0) atomicCAS(p.status, 0, -1);
-          tma_load_4d(dst + s * T::SLICE_BYTES, tmK, bar, 0, y, 0, z);
-          tma_load_4d(dst + T::HALF_BYTES + s * T::SLICE_BYTES, tmV, bar, 0, y, 0, z);
-        }
-        __syncwarp();
+        z[s] = page < p.n_pages ? page * p.H_kv + t.w.h : -1;
       }
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, __popc(have) * 2 * T::SLICE_BYTES);
+#pragma unroll
+        for (int s = 0; s < PD_WARPS; ++s) {
+          if (!((have >> s) & 1u)) continue;
+          const int y = (y0 + s * PD_SLICE) & ((1 << p.page_shift) - 1);
+          tma_load_4d(dst + s * T::SLICE_BYTES, tmK, bar, 0, y, 0, z[s]);
+          tma_load_4d(dst + T::HALF_BYTES + s * T::SLICE_BYTES, tmV, bar, 0, y, 0, z[s]);
+        }
+      }
+      __syncwarp();
       ++issued;
       if (++stage == T::NST) {
         stage = 0;
@@ -542,15 +573,24 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  grid_dependency_wait();
+  // Behind a shared prefix the launch before is the prefix's, whose CTAs had
+  // passed their dependency wait when this one was launched: what came before
+  // that is complete, and nothing here reads what the prefix's launch writes.
+  // So the two run side by side, and only the last CTA waits, at its end, so
+  // that this launch is not complete before the other one.
+  const bool late = p.shared_tiles > 0 && !p.prefix;
+  if (!late) grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
 
   const int HR = p.H_kv * p.row_tiles;
   const PdSum sum = pd_sum<PD_THREADS>(p, part, lens_s);
-  const PdCut cut = pd_cut(sum.total * HR, gridDim.x);
+  const PdCut cut = pd_cut(sum.total * HR, sum.ranges);
   if (static_cast<int>(blockIdx.x) >= cut.n) {
-    if (warp == PD_WARPS) pd_report_lens(p);
+    if (warp == PD_WARPS) {
+      pd_report_lens(p);
+      if (late && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
+    }
     return;
   }
   PdWalk w;
@@ -566,6 +606,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     if (!p.withhold_loads)   // failure-detection test: every wait on a tile runs out
       pd_load_role<D, NT>(p, w, &tmK, &tmV, ring, q_tile, full, empty, q_full, q_empty, lens_s, lane, abort_flag);
     pd_report_lens(p);
+    if (late && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
     return;
   }
 
@@ -909,6 +950,13 @@ __device__ __forceinline__ PdParts pd_parts(const PdParams& p, const PdCut& cut,
   return x;
 }
 
+// The same of a row r further on in the group.
+__device__ __forceinline__ PdParts pd_row_on(PdParts x, int r) {
+  x.row += r;
+  x.row_next += r;
+  return x;
+}
+
 __device__ __forceinline__ size_t pd_part_row(const PdParts& x, int s) {
   return s == 0 ? x.row : x.row_next + static_cast<size_t>(s - 1) * x.step;
 }
@@ -1020,21 +1068,21 @@ __device__ __forceinline__ void pd_write_empty(const PdParams& p, int b) {
     for (int i = threadIdx.x; i < rows; i += PD_MERGE) p.lse[row0 + i] = -INFINITY;
 }
 
-// Without a shared prefix: CTA c takes the group that the boundary behind
-// range c cuts, if any, and of it the share that falls to it among the
-// boundaries that cut the same group.
+// Without a shared prefix: CTAs c, c + ranges, ... (`subs` of them) take the
+// group that the boundary behind range c cuts, if any, and of it the share that
+// falls to them among the boundaries that cut the same group.
 //
 // Both merging kernels may read the lengths before their dependency wait: every
 // CTA of the attending kernel had passed its own when this one was launched,
 // so what ran before that kernel is complete, and it writes no lengths.
 template <int D, bool BF16, bool OUT_F32>
 __global__ void __launch_bounds__(PD_MERGE)
-attn_paged_merge(const PdParams p) {
+attn_paged_merge(const PdParams p, int subs) {
   __shared__ int part[PD_MERGE / 32 + 2];
   const int HR = p.H_kv * p.row_tiles;
   const PdSum sum = pd_sum<PD_MERGE>(p, part, nullptr);
   const PdCut cut = pd_cut(sum.total * HR, p.ranges);
-  const int c = blockIdx.x;
+  const int c = blockIdx.x % p.ranges, sub = blockIdx.x / p.ranges;
   PdWalk w;
   bool any = c + 1 < cut.n;
   int c_first = 0, cuts = 1, g_start = 0;
@@ -1063,11 +1111,12 @@ attn_paged_merge(const PdParams p) {
   // threads share a row's parts; else each takes rows of its own.
   constexpr int SETS = PD_MERGE / (D / 4);
   const int set = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
-  const int mine = c - c_first;
-  if (cuts + 1 > 8 && n_rows <= 2 * cuts) {
+  const int mine = (c - c_first) * subs + sub, takers = cuts * subs;
+  const PdParts parts = pd_parts(p, cut, g_start, w.s.tiles, 0, 0);
+  if (parts.n > 8 && n_rows <= 2 * takers) {
     __shared__ PdMix mix[PD_MERGE];
-    for (int r = mine; r < n_rows; r += cuts) {
-      PdMix x = pd_mix<D>(c4, pd_parts(p, cut, g_start, w.s.tiles, 0, r), none, set, SETS);
+    for (int r = mine; r < n_rows; r += takers) {
+      PdMix x = pd_mix<D>(c4, pd_row_on(parts, r), none, set, SETS);
       mix[threadIdx.x] = x;
       __syncthreads();
       if (set == 0) {
@@ -1078,9 +1127,8 @@ attn_paged_merge(const PdParams p) {
       __syncthreads();
     }
   } else {
-    for (int r = mine * SETS + set; r < n_rows; r += cuts * SETS)
-      pd_write_mix<D, BF16, OUT_F32>(
-          p, idx0 + r, c4, pd_mix<D>(c4, pd_parts(p, cut, g_start, w.s.tiles, 0, r), none, 0, 1));
+    for (int r = mine * SETS + set; r < n_rows; r += takers * SETS)
+      pd_write_mix<D, BF16, OUT_F32>(p, idx0 + r, c4, pd_mix<D>(c4, pd_row_on(parts, r), none, 0, 1));
   }
 }
 
@@ -1105,7 +1153,7 @@ attn_paged_merge_shared(const PdParams p, const PdParams pre) {
   pd_scan<PD_MERGE>(x, part, before);
   pd_scan<PD_MERGE>(all, part, total);
   const PdCut cut = pd_cut(total * HR, p.ranges);
-  const PdCut p_cut = pd_cut(pre.shared_tiles * pre.H_kv * pre.row_tiles, pre.ranges);
+  const PdCut p_cut = pd_cut(pre.shared_tiles * pre.H_kv * pre.row_tiles, pd_prefix_ranges(pre, total * HR));
   int b = b0;
   PdSeq s = pd_seq(p, pd_len_of(p, b));
   const int set = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);

@@ -7,8 +7,10 @@
 //
 // How: the rows are the A operand of S = Q K^T on the 5th-generation tensor
 // cores (tcgen05.mma, one row a TMEM lane); P is written over S in TMEM and O +=
-// P V reads it from there.  K and V tiles come page by page, by TMA, through a
-// ring of shared-memory stages.  Two softmax warpgroups work in turn, so that
+// P V reads it from there.  K and V tiles come page by page, one TMA load each,
+// through a ring of shared-memory stages.  A tile lies in groups of 8 rows, each
+// the 64-column chunks of its rows one behind the other (swizzled), so that a
+// page of any size is one box and the groups of a tile are evenly spaced.  Two softmax warpgroups work in turn, so that
 // one's softmax runs beside the other's products:
 //   PAIR   (groups of 256 rows) each takes 128 rows and every tile, so that a
 //          tile loaded feeds two pairs of products;
@@ -33,6 +35,7 @@ struct PtGeo {
   using G = Geo<D>;                                     // 64-column chunks, 128-byte swizzle
   static constexpr int NST = D == 64 ? 4 : (PAIR ? 2 : 3);   // K/V ring stages
   static constexpr int M = PAIR ? 256 : 128;            // query rows of a group
+  static constexpr int GROUP_BYTES = G::NCH * 1024;     // 8 rows of a K or V tile
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + (PAIR ? 2 : 1) * G::TILE_BYTES;
   static constexpr int V_OFF = K_OFF + NST * G::TILE_BYTES;
@@ -90,10 +93,8 @@ __device__ void pt_tma_role(const PdParams& p, PdWalk w, const CUtensorMap* tmK,
   const int box = min(1 << p.page_shift, PT_TILE);     // rows of one load
   const int boxes = PT_TILE / box;                      // a power of two, at most 8
   const int bshift = 31 - __clz(boxes);
-  int stage = 0;
-  uint32_t ph = 1;                                      // parity of the empty barriers
-  int k_last[T::NST], v_last[T::NST];
-  for (int s = 0; s < T::NST; ++s) k_last[s] = v_last[s] = -1;
+  uint32_t stage = 0, ph = 1;                           // parity of the empty barriers
+  uint32_t issued[2] = {0, 0};                          // tiles of K and of V
   bool ok = true;
   auto wait = [&](uint32_t bar, uint32_t par) {
     const bool x = mbar_try_wait(bar, par) || wait_slow(bar, par, abort_flag, p.status, p.watchdog_ns);
@@ -101,9 +102,9 @@ __device__ void pt_tma_role(const PdParams& p, PdWalk w, const CUtensorMap* tmK,
   };
   for (bool more = true; more && ok; more = pd_next_run(p, w, nullptr)) {
     const int* row = p.table + (p.prefix ? 0 : static_cast<size_t>(w.b) * p.max_pages);
-    int l_base = 0, l_page = -2;                        // pages of 32 boxes, from tile l_base on
+    int l_base = -32, l_page = -1;                      // pages of 32 boxes, from tile l_base on
     for (int i = w.i0; i < w.i_end && ok; ++i) {
-      if (l_page == -2 || i >= l_base + (32 >> bshift)) {
+      if (i >= l_base + (32 >> bshift)) {
         l_base = i;
         const int li = i + (lane >> bshift);
         l_page = -1;
@@ -117,32 +118,30 @@ __device__ void pt_tma_role(const PdParams& p, PdWalk w, const CUtensorMap* tmK,
           }
         }
       }
-      const int c0 = pd_tile_key(p, w.s, i);
       const int first = (i - l_base) << bshift;         // lane of the tile's first box
       const uint32_t have = __ballot_sync(0xffffffffu, l_page >= 0) >> first & ((1u << boxes) - 1);
-      const int bytes = __popc(have) * box * D * 2;
+      const int u0 = (pd_tile_key(p, w.s, i) & ((1 << p.page_shift) - 1)) >> 3;   // group of the page
+      int z[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int page = __shfl_sync(0xffffffffu, l_page, (first + x) & 31);
+        z[x] = page < p.n_pages ? page * p.H_kv + w.h : -1;
+      }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t full = bars + 8 * ((kv ? P_V_FULL : P_K_FULL) + stage);
         const uint32_t dst = sbase + (kv ? T::V_OFF : T::K_OFF) + stage * G::TILE_BYTES;
         ok = ok && wait(bars + 8 * ((kv ? P_V_EMPTY : P_K_EMPTY) + stage), ph);
         if (!ok) break;
-        if (elect_one()) mbar_arrive_expect_tx(full, bytes);
-        __syncwarp();
-        // the whole warp goes through the boxes, one elected lane issues
-        for (int x = 0; x < boxes; ++x) {
-          const int page = __shfl_sync(0xffffffffu, l_page, first + x);
-          if (page < 0) continue;
-          const int z = page < p.n_pages ? page * p.H_kv + w.h : -1;
-          const int y = (c0 + x * box) & ((1 << p.page_shift) - 1);
-          if (elect_one()) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full, __popc(have) * box * D * 2);
+          // boxes of one tile lie in different pages, or are one (u0 is then its place there)
 #pragma unroll
-            for (int c = 0; c < G::NCH; ++c)
-              tma_load_3d(dst + c * G::CHUNK_BYTES + x * box * 128, kv ? tmV : tmK, full, c * 64, y, z);
-          }
-          __syncwarp();
+          for (int x = 0; x < 8; ++x)
+            if ((have >> x) & 1u) tma_load_5d(dst + x * box * D * 2, kv ? tmV : tmK, full, 0, 0, 0, x == 0 ? u0 : 0, z[x]);
         }
-        (kv ? v_last : k_last)[stage] = static_cast<int>(ph ^ 1u);
+        __syncwarp();
+        ++issued[kv];
       }
       if (++stage == T::NST) {
         stage = 0;
@@ -150,11 +149,12 @@ __device__ void pt_tma_role(const PdParams& p, PdWalk w, const CUtensorMap* tmK,
       }
     }
   }
+  // after an expired wait, the copies still in flight
   if (!ok) {
-    for (int s = 0; s < T::NST; ++s) {
-      if (k_last[s] >= 0) drain_wait(bars + 8 * (P_K_FULL + s), k_last[s], p.watchdog_ns);
-      if (v_last[s] >= 0) drain_wait(bars + 8 * (P_V_FULL + s), v_last[s], p.watchdog_ns);
-    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      for (uint32_t i = issued[kv] > T::NST ? issued[kv] - T::NST : 0; i < issued[kv]; ++i)
+        drain_wait(bars + 8 * ((kv ? P_V_FULL : P_K_FULL) + i % T::NST), (i / T::NST) & 1u, p.watchdog_ns);
   }
 }
 
@@ -178,9 +178,10 @@ __device__ void pt_mma_role(const PdParams& p, PdWalk w, uint32_t tmem, uint32_t
     const uint32_t ka = sbase + T::K_OFF + s * G::TILE_BYTES;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      const uint32_t off = (kk * 16 / G::CW) * G::CHUNK_BYTES + ((kk * 16) % G::CW) * 2;
-      mma_ss(tmem + T::S_COL0 + h * PT_TILE, smem_desc(qa + off, 16, 8 * G::CB, G::LAYOUT),
-             smem_desc(ka + off, 16, 8 * G::CB, G::LAYOUT), idesc_qk, kk > 0 ? 1u : 0u);
+      const uint32_t in = ((kk * 16) % G::CW) * 2;
+      mma_ss(tmem + T::S_COL0 + h * PT_TILE,
+             smem_desc(qa + (kk * 16 / G::CW) * G::CHUNK_BYTES + in, 16, 8 * G::CB, G::LAYOUT),
+             smem_desc(ka + (kk * 16 / G::CW) * 1024 + in, 16, T::GROUP_BYTES, G::LAYOUT), idesc_qk, kk > 0 ? 1u : 0u);
     }
   };
   auto issue_o = [&](int h, int s, bool acc) {
@@ -188,7 +189,7 @@ __device__ void pt_mma_role(const PdParams& p, PdWalk w, uint32_t tmem, uint32_t
 #pragma unroll
     for (int kk = 0; kk < PT_TILE / 16; ++kk)
       mma_ts(tmem + T::O_COL0 + h * D, tmem + T::S_COL0 + h * PT_TILE + kk * 8,
-             smem_desc(va + kk * 16 * G::CB, G::CHUNK_BYTES, 8 * G::CB, G::LAYOUT), idesc_pv,
+             smem_desc(va + kk * 2 * T::GROUP_BYTES, 1024, T::GROUP_BYTES, G::LAYOUT), idesc_pv,
              (acc || kk > 0) ? 1u : 0u);
   };
   // S of item k, once its K tile (and, first, the warpgroup's rows) is there
@@ -269,7 +270,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
       const uint32_t row_addr = sbase + T::Q_OFF + (PAIR ? h : 0) * G::TILE_BYTES + L * 128;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
                                                         (real ? pd_row_index(p, w, r) : 0) * D);
-#pragma unroll
+#pragma unroll 8
       for (int u = 0; u < D / 8; ++u) {
         uint4 x = real ? src[u] : make_uint4(0u, 0u, 0u, 0u);
         st_shared_v4(row_addr + (u / 8) * G::CHUNK_BYTES + (((u % 8) ^ (L & 7)) << 4), x.x ^ q_sign, x.y ^ q_sign,
@@ -301,7 +302,9 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
       tc_fence_after_sync();
       // S is read twice, 64 columns at a time: for its maximum, then for P.
       // Held in registers at once, its 128 columns left too few for the rest
-      // (spills: 3 us a tile instead of 0.6).
+      // (spills: 3 us a tile instead of 1).  The loops here and in the epilogue
+      // are not unrolled: each launch fetches the code anew, and a first tile
+      // took 6000 cycles where a later one takes 2200.
       const bool masked = c0 + PT_TILE - 1 > hi_min ||
                           (p.window > 0 && c0 < lo_max && c0 + PT_TILE > p.n_sink);
       uint32_t sa[32], sb[32];
@@ -320,7 +323,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
         }
       };
       float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         fetch(64 * half);
 #pragma unroll
@@ -355,7 +358,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
         }
         tmem_st_32x32b_x16(s_tmem + col, pk);
       };
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         fetch(64 * half);
         weights(sa, 32 * half);
@@ -367,7 +370,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
         // O_h holds the earlier tiles (their P V completed before the S product
         // of this tile was issued)
         const uint32_t o_tmem = tmem + lane_base + T::O_COL0 + h * D;
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t orr[32];
           tmem_ld_32x32b_x32(o_tmem + cc * 32, orr);
@@ -385,9 +388,9 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
         if (!ok) break;
         const int key = c0 + L;
         if (!(key < used.len && (key >= used.lo || key < p.n_sink))) {
-          const uint32_t v_row = sbase + T::V_OFF + s * G::TILE_BYTES + L * 128;
-#pragma unroll
-          for (int u = 0; u < D / 8; ++u) st_shared_v4(v_row + (u / 8) * G::CHUNK_BYTES + (u % 8) * 16, 0u, 0u, 0u, 0u);
+          const uint32_t v_row = sbase + T::V_OFF + s * G::TILE_BYTES + (L >> 3) * T::GROUP_BYTES + (L & 7) * 128;
+#pragma unroll 1
+          for (int u = 0; u < D / 8; ++u) st_shared_v4(v_row + (u / 8) * 1024 + (u % 8) * 16, 0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
@@ -450,7 +453,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
       row += (static_cast<size_t>(w.b) * HR + w.h * p.row_tiles + w.rt) * T::M;
     float* po = split ? p.part_o : p.own_o;
     float* pl = split ? p.part_lse : p.own_lse;
-#pragma unroll
+#pragma unroll 1
     for (int cc = 0; cc < D / 16; ++cc) {
       uint32_t o0[16], o1[16];
       tmem_ld_32x32b_x16(tmem + lane_base + T::O_COL0 + (PAIR ? h * D : 0) + cc * 16, o0);
@@ -526,7 +529,9 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
   // The set-up above touches no global memory, so it may overlap the end of
   // the previous grid of the stream; nothing below runs before that grid is done.
-  grid_dependency_wait();
+  // (Behind a shared prefix: see attn_paged_kernel.)
+  const bool late = p.shared_tiles > 0 && !p.prefix;
+  if (!late) grid_dependency_wait();
   grid_launch_dependents();
   tc_fence_before_sync();
   __syncthreads();
@@ -541,7 +546,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     if (lane == 0) atomicMax(longest_s, n);
   }
   if (warp == NUM_THREADS / 32 - 1) pd_report_lens(p);
-  const PdCut cut = pd_cut(sum.total * HR, gridDim.x);
+  const PdCut cut = pd_cut(sum.total * HR, sum.ranges);
   const bool any = static_cast<int>(blockIdx.x) < cut.n;
   PdWalk w;
   const int f0 = any ? pd_start(cut, blockIdx.x) : 0;
@@ -576,6 +581,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     if (warp == MMA_WARP) {
       tc_fence_after_sync();
       tmem_dealloc(tmem, TMEM_COLS);
+      if (late && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
     }
   }
 }
