@@ -20,9 +20,14 @@ struct PagedForm {
   int weight;   // 100 cycles of an SM a tile
 };
 
-PagedForm paged_form(long long rows) {
+// Up to 16 rows attn_paged_kernel, whose products are of 8 rows: 8 sequences
+// of up to 8192, 16 rows, d = 128 take 50 us (with 128-row products 46), 64 of
+// up to 256 take 44 us (54).  At d = 64, where a 128-row tile's exponentials
+// take longer than HBM does, up to 32 rows in two groups: 34 us (37), 17 (18);
+// at d = 128 those take 67 us (47).
+PagedForm paged_form(long long rows, int d) {
   PagedForm f;
-  f.m = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+  f.m = rows <= 8 ? 8 : rows <= (d == 64 ? 32 : 16) ? 16 : rows <= 128 ? 128 : 256;
   f.row_tiles = static_cast<int>((rows + f.m - 1) / f.m);
   f.tile_shift = f.m <= 16 ? 6 : 7;
   f.ranges = f.m <= 16 ? 296 : 148;
@@ -59,11 +64,11 @@ PagedPlan paged_plan(int B, int H, int H_kv, int N_q, int d, int shared_len) {
   PagedPlan pl{};
   const long long R = static_cast<long long>(H / H_kv) * N_q;
   pl.shared = shared_len >= kSharedUnit;
-  pl.form = paged_form(R);
+  pl.form = paged_form(R, d);
   pl.own = paged_space(0, pl.form, pl.shared ? static_cast<size_t>(B) * H_kv * pl.form.row_tiles : 0, d);
   pl.bytes = pl.own.end;
   if (pl.shared) {
-    pl.prefix_form = paged_form(B * R);
+    pl.prefix_form = paged_form(B * R, d);
     pl.prefix = paged_space(pl.own.end, pl.prefix_form, static_cast<size_t>(H_kv) * pl.prefix_form.row_tiles, d);
     pl.bytes = pl.prefix.end;
   }

@@ -716,20 +716,21 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         if (lane == 0) mbar_arrive(free_bar);
         continue;
       }
-      // S^T, the even and the odd steps of d summed apart (two chains)
-      float s[NT][4] = {}, s2[NT][4] = {};
+      // S^T in two chains of products: for 8 rows, the even and the odd steps of
+      // d summed apart
+      float s[2][4] = {};
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t kf[4];
         pd_ldsm(ks + (k >> 2) * T::CHUNK_BYTES + k_off[k & 3], kf);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) pd_mma<BF16>((k & 1) ? s2[n] : s[n], kf, qf[k][n][0], qf[k][n][1]);
+        for (int n = 0; n < NT; ++n) pd_mma<BF16>(s[NT == 1 ? k & 1 : n], kf, qf[k][n][0], qf[k][n][1]);
       }
       bool up = false;
+      if constexpr (NT == 1) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+        for (int e = 0; e < 4; ++e) s[0][e] += s[1][e];
+      }
       const bool masked = key0 + PD_SLICE - 1 > hi_min ||
                           (p.window > 0 && key0 < lo_max && key0 + PD_SLICE > p.n_sink);
       if (masked) {
