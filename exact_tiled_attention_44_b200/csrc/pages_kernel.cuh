@@ -16,6 +16,8 @@
 namespace attn {
 
 constexpr int PG_PLAN_THREADS = 1024;   // the deciding kernels: one CTA
+constexpr int PG_LIST = 4096;           // free pages kept in shared memory
+constexpr int PG_FEW = 4;               // pages one thread hands out to a sequence
 constexpr int PG_THREADS = 256;         // the moving kernels
 constexpr int PG_ROWS = 64;             // new rows of one (sequence, K/V head) a CTA writes
 constexpr int PG_CHUNK = PG_THREADS * 16 * 4;   // bytes of a page a CTA moves at a time
@@ -75,6 +77,25 @@ __device__ __forceinline__ int pg_scan(int x, int* part, int& total) {
   return before;
 }
 
+// Which of the 16 pages from `first` on have no reference (bit u: page first + u).
+__device__ __forceinline__ uint32_t pg_zero_bits(const Pages& p, int first) {
+  uint32_t bits = 0;
+  if (first + 16 <= p.n_pages && (reinterpret_cast<uintptr_t>(p.refs) & 15u) == 0) {
+    const int4* r4 = reinterpret_cast<const int4*>(p.refs + first);
+    int4 r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] = r4[u];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      bits |= ((r[u].x <= 0 ? 1u : 0u) | (r[u].y <= 0 ? 2u : 0u) | (r[u].z <= 0 ? 4u : 0u) |
+               (r[u].w <= 0 ? 8u : 0u)) << (4 * u);
+  } else {
+    for (int u = 0; u < 16; ++u)
+      if (first + u < p.n_pages && p.refs[first + u] <= 0) bits |= 1u << u;
+  }
+  return bits;
+}
+
 // ------------------------------------------------------------ append
 
 // What attn_pages_append's first kernel hands to its second, for each
@@ -97,7 +118,7 @@ struct AppendPlan {
 // that cannot be served and every later one that needs pages get none.
 __global__ void __launch_bounds__(PG_PLAN_THREADS)
 attn_pages_append_plan(const Pages p, const AppendPlan a, const int* counts, int n_new) {
-  __shared__ int part[33];
+  __shared__ int part[33], list_s[PG_LIST];
   grid_dependency_wait();
   grid_launch_dependents();
   const int t = threadIdx.x;
@@ -134,55 +155,64 @@ attn_pages_append_plan(const Pages p, const AppendPlan a, const int* counts, int
     if (b < p.B) a.base[b] = wanted + before;
     wanted += total;
   }
-  // the lowest `wanted` free pages: 16 counts a thread and step
+  // the lowest `wanted` free pages, 16 counts a thread and step; few of them
+  // stay in shared memory
+  int* list = wanted <= PG_LIST ? list_s : a.free_list;
   int found = 0;
   for (int c0 = 0; found < wanted && c0 < p.n_pages; c0 += PG_PLAN_THREADS * 16) {
     const int first = c0 + t * 16;
-    uint32_t free_bits = 0;
-    if (first + 16 <= p.n_pages && (reinterpret_cast<uintptr_t>(p.refs) & 15u) == 0) {
-      const int4* r4 = reinterpret_cast<const int4*>(p.refs + first);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int4 r = r4[u];
-        free_bits |= ((r.x == 0 ? 1u : 0u) | (r.y == 0 ? 2u : 0u) | (r.z == 0 ? 4u : 0u) |
-                      (r.w == 0 ? 8u : 0u)) << (4 * u);
-      }
-    } else {
-      for (int u = 0; u < 16; ++u)
-        if (first + u < p.n_pages && p.refs[first + u] == 0) free_bits |= 1u << u;
-    }
+    uint32_t free_bits = pg_zero_bits(p, first);
     int total;
     int k = found + pg_scan(__popc(free_bits), part, total);
     for (; free_bits != 0 && k < wanted; free_bits &= free_bits - 1, ++k)
-      a.free_list[k] = first + __ffs(free_bits) - 1;
+      list[k] = first + __ffs(free_bits) - 1;
     found += total;
   }
-  __syncthreads();   // base, need, from and the free list are this CTA's own writes
-  // one warp a sequence: hand out the pages
+  __syncthreads();   // need, base, from and the list are this CTA's own writes
+  // hand them out: a thread a sequence, a warp together for those of many pages
   const int lane = t & 31;
-  for (int b = t >> 5; b < p.B; b += PG_PLAN_THREADS / 32) {
-    const int need = a.need[b], base = a.base[b], start = a.start[b], c = a.count[b], from = a.from[b];
-    if (need > 0 && static_cast<long long>(base) + need > found) {
-      if (lane == 0) {
+  for (int b0 = 0; b0 < p.B; b0 += PG_PLAN_THREADS) {
+    const int b = b0 + t;
+    int need = 0, base = 0, col0 = 0;
+    if (b < p.B) {
+      need = a.need[b];
+      base = a.base[b];
+      const int start = a.start[b], c = a.count[b], from = a.from[b];
+      if (need > 0 && static_cast<long long>(base) + need > found) {
         pg_report(p, STATUS_NO_PAGES);
         a.count[b] = 0;
         a.from[b] = -1;
-      }
-      continue;
-    }
-    // column of the first page handed out: the copied one's, or the next free column
-    const int col0 = from >= 0 ? start >> p.page_shift : pg_count(p, start);
-    int* row = p.table + static_cast<size_t>(b) * p.max_pages;
-    for (int j = lane; j < need; j += 32) {
-      const int page = a.free_list[base + j];
-      row[col0 + j] = page;
-      p.refs[page] = 1;
-      if (from >= 0 && j == 0) {
-        a.to[b] = page;
-        atomicSub(&p.refs[from], 1);
+        need = 0;
+      } else if (c > 0) {
+        p.lens[b] = start + c;
+        // column of the first page handed out: the copied one's, or the next free column
+        col0 = from >= 0 ? start >> p.page_shift : pg_count(p, start);
+        if (from >= 0) {
+          a.to[b] = list[base];
+          atomicSub(&p.refs[from], 1);
+        }
       }
     }
-    if (lane == 0 && c > 0) p.lens[b] = start + c;
+    int* row = p.table + static_cast<size_t>(b) * p.max_pages + col0;
+    if (need <= PG_FEW) {
+#pragma unroll
+      for (int j = 0; j < PG_FEW; ++j)
+        if (j < need) {
+          const int page = list[base + j];
+          row[j] = page;
+          p.refs[page] = 1;
+        }
+    }
+    for (uint32_t many = __ballot_sync(0xffffffffu, need > PG_FEW); many != 0; many &= many - 1) {
+      const int l = __ffs(many) - 1;
+      const int n = __shfl_sync(0xffffffffu, need, l), first = __shfl_sync(0xffffffffu, base, l);
+      int* to = reinterpret_cast<int*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), l));
+      for (int j = lane; j < n; j += 32) {
+        const int page = list[first + j];
+        to[j] = page;
+        p.refs[page] = 1;
+      }
+    }
   }
 }
 
@@ -351,54 +381,25 @@ attn_pages_compact_plan(const Pages p, const CompactPlan a, int* n_live_out) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int t = threadIdx.x;
-  const bool vec = (reinterpret_cast<uintptr_t>(p.refs) & 15u) == 0;
   int live = 0;
-  for (int first = t * 4; first < p.n_pages; first += PG_PLAN_THREADS * 4) {
-    if (vec && first + 4 <= p.n_pages) {
-      const int4 r = *reinterpret_cast<const int4*>(p.refs + first);
-      live += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
-    } else {
-      for (int u = first; u < first + 4 && u < p.n_pages; ++u) live += p.refs[u] > 0;
-    }
-  }
+  for (int first = t * 16; first < p.n_pages; first += PG_PLAN_THREADS * 16)
+    live += min(16, p.n_pages - first) - __popc(pg_zero_bits(p, first));
+  for (int page = t; page < p.n_pages; page += PG_PLAN_THREADS) a.map[page] = page;
   int n_live;
   pg_scan(live, part, n_live);
   int moved = 0, filled = 0;
-  for (int c0 = 0; c0 < p.n_pages; c0 += PG_PLAN_THREADS * 4) {
-    const int first = c0 + t * 4;
-    int n_src = 0, n_dst = 0;
-    int r[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) r[u] = 0;
-    if (vec && first + 4 <= p.n_pages) {
-      const int4 q = *reinterpret_cast<const int4*>(p.refs + first);
-      r[0] = q.x; r[1] = q.y; r[2] = q.z; r[3] = q.w;
-    } else {
-      for (int u = 0; u < 4; ++u)
-        if (first + u < p.n_pages) r[u] = p.refs[first + u];
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int page = first + u;
-      if (page >= p.n_pages) continue;
-      if (page < n_live) n_dst += r[u] <= 0;
-      else n_src += r[u] > 0;
-    }
-    // at most 4 a thread and 4096 a step: both counts fit one 32-bit scan
+  for (int c0 = 0; c0 < p.n_pages; c0 += PG_PLAN_THREADS * 16) {
+    const int first = c0 + t * 16;
+    const int n = max(0, min(16, p.n_pages - first));
+    const uint32_t all = (1u << n) - 1u, zero = pg_zero_bits(p, first);
+    const int below = max(0, min(n, n_live - first));              // pages of these below n_live
+    uint32_t dst = zero & ((1u << below) - 1u), src = ~zero & all & ~((1u << below) - 1u);
+    // at most 16 a thread and 16384 a step: both counts fit one 32-bit scan
     int total;
-    const int both = pg_scan(n_src << 16 | n_dst, part, total);
+    const int both = pg_scan(__popc(src) << 16 | __popc(dst), part, total);
     int s = moved + (both >> 16), d = filled + (both & 0xffff);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int page = first + u;
-      if (page >= p.n_pages) continue;
-      a.map[page] = page;
-      if (page < n_live) {
-        if (r[u] <= 0) a.dst[d++] = page;
-      } else if (r[u] > 0) {
-        a.src[s++] = page;
-      }
-    }
+    for (; src != 0; src &= src - 1) a.src[s++] = first + __ffs(src) - 1;
+    for (; dst != 0; dst &= dst - 1) a.dst[d++] = first + __ffs(dst) - 1;
     moved += total >> 16;
     filled += total & 0xffff;
   }
