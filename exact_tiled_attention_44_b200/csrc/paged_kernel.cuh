@@ -147,9 +147,11 @@ __device__ __forceinline__ void pd_report_lens(const PdParams& p) {
 }
 
 // F tiles in `n` ranges: the first `more` ranges have one tile more than the
-// other `each`.
+// other `each`.  With k > 0 every group of `tiles` tiles is cut into k ranges of
+// its own instead.
 struct PdCut {
   int n, each, more;
+  int k, tiles;
 };
 
 __device__ __forceinline__ PdCut pd_cut(int F, int n) {
@@ -157,13 +159,39 @@ __device__ __forceinline__ PdCut pd_cut(int F, int n) {
   c.n = min(F, n);
   c.each = F / max(c.n, 1);
   c.more = F - c.each * c.n;
+  c.k = 0;
+  c.tiles = 0;
   return c;
 }
 
-__device__ __forceinline__ int pd_start(const PdCut& c, int i) { return i * c.each + min(i, c.more); }
+// A prefix's groups are all of one length, so where there are at least as many
+// ranges (a run that begins in mid-range costs 18000 cycles, four tiles) no
+// range holds parts of two.
+__device__ __forceinline__ PdCut pd_cut_prefix(const PdParams& pre, int n) {
+  const int groups = pre.H_kv * pre.row_tiles;
+  PdCut c = pd_cut(groups * pre.shared_tiles, n);
+  if (pre.m > 16 && n >= groups) {
+    c.k = min(n / groups, pre.shared_tiles);
+    c.tiles = pre.shared_tiles;
+    c.n = c.k * groups;
+  }
+  return c;
+}
+
+__device__ __forceinline__ int pd_start(const PdCut& c, int i) {
+  if (c.k > 0) {
+    const int g = i / c.k;
+    return g * c.tiles + (i - g * c.k) * c.tiles / c.k;
+  }
+  return i * c.each + min(i, c.more);
+}
 
 // The range that holds tile f.
 __device__ __forceinline__ int pd_range_of(const PdCut& c, int f) {
+  if (c.k > 0) {
+    const int g = f / c.tiles;
+    return g * c.k + ((f - g * c.tiles + 1) * c.k - 1) / c.tiles;
+  }
   const int t = c.more * (c.each + 1);
   return f < t ? f / (c.each + 1) : c.more + (f - t) / c.each;
 }
@@ -585,7 +613,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
   const int HR = p.H_kv * p.row_tiles;
   const PdSum sum = pd_sum<PD_THREADS>(p, part, lens_s);
-  const PdCut cut = pd_cut(sum.total * HR, sum.ranges);
+  const PdCut cut = p.prefix ? pd_cut_prefix(p, sum.ranges) : pd_cut(sum.total * HR, sum.ranges);
   if (static_cast<int>(blockIdx.x) >= cut.n) {
     if (warp == PD_WARPS) {
       pd_report_lens(p);
@@ -1154,7 +1182,7 @@ attn_paged_merge_shared(const PdParams p, const PdParams pre) {
   pd_scan<PD_MERGE>(x, part, before);
   pd_scan<PD_MERGE>(all, part, total);
   const PdCut cut = pd_cut(total * HR, p.ranges);
-  const PdCut p_cut = pd_cut(pre.shared_tiles * pre.H_kv * pre.row_tiles, pd_prefix_ranges(pre, total * HR));
+  const PdCut p_cut = pd_cut_prefix(pre, pd_prefix_ranges(pre, total * HR));
   int b = b0;
   PdSeq s = pd_seq(p, pd_len_of(p, b));
   const int set = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);

@@ -270,7 +270,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
       const uint32_t row_addr = sbase + T::Q_OFF + (PAIR ? h : 0) * G::TILE_BYTES + L * 128;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
                                                         (real ? pd_row_index(p, w, r) : 0) * D);
-#pragma unroll 8
+#pragma unroll
       for (int u = 0; u < D / 8; ++u) {
         uint4 x = real ? src[u] : make_uint4(0u, 0u, 0u, 0u);
         st_shared_v4(row_addr + (u / 8) * G::CHUNK_BYTES + (((u % 8) ^ (L & 7)) << 4), x.x ^ q_sign, x.y ^ q_sign,
@@ -546,7 +546,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     if (lane == 0) atomicMax(longest_s, n);
   }
   if (warp == NUM_THREADS / 32 - 1) pd_report_lens(p);
-  const PdCut cut = pd_cut(sum.total * HR, sum.ranges);
+  const PdCut cut = p.prefix ? pd_cut_prefix(p, sum.ranges) : pd_cut(sum.total * HR, sum.ranges);
   const bool any = static_cast<int>(blockIdx.x) < cut.n;
   PdWalk w;
   const int f0 = any ? pd_start(cut, blockIdx.x) : 0;
