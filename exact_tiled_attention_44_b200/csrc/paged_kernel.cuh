@@ -448,27 +448,26 @@ __device__ __forceinline__ void pd_sync_attending() {
 }
 
 // Up to PD_BATCH tiles of a run, and in lane 4 j + s the page of slice s of
-// its j-th tile (-1: the slice is not loaded; n_pages: the entry is bad, so the
-// box lies outside the tensor and is filled with zeros).
+// its j-th tile, if that slice is to be loaded.  The page is not looked at
+// before its batch is loaded, so the table's latency is spent on the batch before.
 constexpr int PD_BATCH = 32 / PD_WARPS;
 
 struct PdBatch {
   PdWalk w;
   int i, n;
+  bool have;
   int page;
 };
 
 __device__ __forceinline__ void pd_look_up(const PdParams& p, PdBatch& t, int lane) {
   t.n = min(PD_BATCH, t.w.i_end - t.i);
-  t.page = -1;
+  t.have = false;
   const int j = lane / PD_WARPS;
   if (j < t.n) {
     const int key = pd_key(t.w.s, t.i + j, lane % PD_WARPS);
-    if (key < t.w.s.len && !pd_gone(p, t.w.s, key)) {
-      const int page = p.table[(p.prefix ? 0 : static_cast<size_t>(t.w.b) * p.max_pages) + (key >> p.page_shift)];
-      t.page = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages) ? page : p.n_pages;
-      if (t.page == p.n_pages) atomicCAS(p.status, 0, -1);
-    }
+    t.have = key < t.w.s.len && !pd_gone(p, t.w.s, key);
+    if (t.have)
+      t.page = p.table[(p.prefix ? 0 : static_cast<size_t>(t.w.b) * p.max_pages) + (key >> p.page_shift)];
   }
 }
 
@@ -489,6 +488,7 @@ __device__ __forceinline__ void pd_load_role(const PdParams& p, const PdWalk& w0
   PdBatch t, next;
   t.w = w0;
   t.i = w0.i0;
+  t.page = 0;
   pd_look_up(p, t, lane);
   bool fresh = true;                                    // t begins a run
   for (bool more = true; more && ok;) {
@@ -513,18 +513,20 @@ __device__ __forceinline__ void pd_load_role(const PdParams& p, const PdWalk& w0
       __syncwarp();
       ++q_issued;
     }
+    // a bad entry's box lies outside the tensor and is filled with zeros
+    const bool good = static_cast<unsigned>(t.page) < static_cast<unsigned>(p.n_pages);
+    const int t_z = good ? t.page * p.H_kv + t.w.h : -1;
+    if (t.have && !good) atomicCAS(p.status, 0, -1);
+    const uint32_t t_have = __ballot_sync(0xffffffffu, t.have);
     for (int j = 0; j < t.n; ++j) {
-      const uint32_t have = __ballot_sync(0xffffffffu, t.page >= 0) >> (j * PD_WARPS) & ((1u << PD_WARPS) - 1);
+      const uint32_t have = t_have >> (j * PD_WARPS) & ((1u << PD_WARPS) - 1);
       ok = wait(empty + 8 * stage, phase);
       if (!ok) break;
       const uint32_t bar = full + 8 * stage, dst = ring + stage * T::STAGE_BYTES;
       const int y0 = pd_tile_key(p, t.w.s, t.i + j) & ((1 << p.page_shift) - 1);
       int z[PD_WARPS];
 #pragma unroll
-      for (int s = 0; s < PD_WARPS; ++s) {
-        const int page = __shfl_sync(0xffffffffu, t.page, j * PD_WARPS + s);
-        z[s] = page < p.n_pages ? page * p.H_kv + t.w.h : -1;
-      }
+      for (int s = 0; s < PD_WARPS; ++s) z[s] = __shfl_sync(0xffffffffu, t_z, j * PD_WARPS + s);
       if (elect_one()) {
         mbar_arrive_expect_tx(bar, __popc(have) * 2 * T::SLICE_BYTES);
 #pragma unroll
