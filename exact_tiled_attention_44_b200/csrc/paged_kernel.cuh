@@ -868,8 +868,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
     // where the result goes: the output, or for a split group the slot of the
     // range's first (0) or of another run (1), or else the group's own place
-    const int g_start = w.x - w.i0;
-    const bool split = pd_range_of(cut, g_start) != pd_range_of(cut, g_start + w.s.tiles - 1);
+    const bool split = w.i_end - w.i0 != w.s.tiles;
     const bool direct = !split && !p.prefix && p.shared_tiles == 0;
     const int n_rows = pd_rows(p, w);
     size_t row;
@@ -921,7 +920,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           o.z = fmaf(wt, y.z, o.z);
           o.w = fmaf(wt, y.w, o.w);
         }
-        const float inv = l_exact == 0.f ? 0.f : 1.f / l_round;
+        const float inv = l_exact == 0.f ? 0.f : __fdividef(1.f, l_round);
         o.x *= inv;
         o.y *= inv;
         o.z *= inv;
@@ -935,7 +934,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
               make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
         if (c4 == 0) {
-          const float z = l_exact == 0.f ? -INFINITY : (top + log2f(l_exact)) * 0.69314718055994531f;
+          const float z = l_exact == 0.f ? -INFINITY : (top + __log2f(l_exact)) * 0.69314718055994531f;
           if (!direct) pl[row + r] = z;
           else if (p.lse != nullptr) p.lse[row + r] = z;
         }
@@ -1040,11 +1039,11 @@ __device__ __forceinline__ PdMix pd_mix(int c4, const PdParts& a, const PdParts&
     }
     if (nan) top = NAN;                          // kept as the maximum, it reaches all that follows
     const float ref = top == -INFINITY ? 0.f : top;
-    pd_scale(x, expf(x.top - ref));              // 0 for the first parts
+    pd_scale(x, __expf(x.top - ref));              // 0 for the first parts
     x.top = top;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float wgt = expf(l[u] - ref);
+      const float wgt = __expf(l[u] - ref);
       x.tot += wgt;
       x.r.x = fmaf(wgt, y[u].x, x.r.x);
       x.r.y = fmaf(wgt, y[u].y, x.r.y);
@@ -1059,8 +1058,8 @@ __device__ __forceinline__ PdMix pd_mix(int c4, const PdParts& a, const PdParts&
 __device__ __forceinline__ void pd_join(PdMix& x, PdMix y) {
   const float top = x.top != x.top || y.top != y.top ? NAN : fmaxf(x.top, y.top);
   const float ref = top == -INFINITY ? 0.f : top;
-  pd_scale(x, expf(x.top - ref));
-  pd_scale(y, expf(y.top - ref));
+  pd_scale(x, __expf(x.top - ref));
+  pd_scale(y, __expf(y.top - ref));
   x.top = top;
   x.tot += y.tot;
   x.r.x += y.r.x;
@@ -1073,7 +1072,7 @@ __device__ __forceinline__ void pd_join(PdMix& x, PdMix y) {
 template <int D, bool BF16, bool OUT_F32>
 __device__ __forceinline__ void pd_write_mix(const PdParams& p, size_t idx, int c4, PdMix x) {
   const bool none = x.top == -INFINITY;
-  const float inv = none ? 0.f : 1.f / x.tot;
+  const float inv = none ? 0.f : __fdividef(1.f, x.tot);
   x.r.x *= inv;
   x.r.y *= inv;
   x.r.z *= inv;
@@ -1084,7 +1083,7 @@ __device__ __forceinline__ void pd_write_mix(const PdParams& p, size_t idx, int 
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + idx * D)[c4] =
         make_uint2(pack2<BF16>(x.r.x, x.r.y), pack2<BF16>(x.r.z, x.r.w));
   }
-  if (c4 == 0 && p.lse != nullptr) p.lse[idx] = none ? -INFINITY : x.top + logf(x.tot);
+  if (c4 == 0 && p.lse != nullptr) p.lse[idx] = none ? -INFINITY : x.top + __logf(x.tot);
 }
 
 // The rows of sequence b, which keeps nothing: zeros and minus infinity.

@@ -438,10 +438,9 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
     const float lr_t = l_round * a0 + lr1 * a1;
     const float le_t = l_exact * a0 + le1 * a1;
     const bool empty = none || le_t == 0.f;
-    const float inv = empty ? 0.f : 1.f / lr_t;
-    const float lse_nat = empty ? -INFINITY : (M + log2f(le_t)) * 0.69314718055994531f;
-    const int g_start = w.x - w.i0;
-    const bool split = pd_range_of(cut, g_start) != pd_range_of(cut, g_start + w.s.tiles - 1);
+    const float inv = empty ? 0.f : __fdividef(1.f, lr_t);
+    const float lse_nat = empty ? -INFINITY : (M + __log2f(le_t)) * 0.69314718055994531f;
+    const bool split = w.i_end - w.i0 != w.s.tiles;
     const bool direct = !split && !p.prefix && p.shared_tiles == 0;
     const int HR = p.H_kv * p.row_tiles;
     size_t row = r;
