@@ -102,6 +102,13 @@ __device__ void pt_tma_role(const PdParams& p, PdWalk w, const CUtensorMap* tmK,
   };
   for (bool more = true; more && ok; more = pd_next_run(p, w, nullptr)) {
     const int* row = p.table + (p.prefix ? 0 : static_cast<size_t>(w.b) * p.max_pages);
+    // the run's query rows are fetched into L2 ahead of the softmax warps, which
+    // read them only when the run before is finished
+    for (int r = lane; r < pd_rows(p, w); r += 32) {
+      const char* q = static_cast<const char*>(p.q) + pd_row_index(p, w, r) * D * 2;
+#pragma unroll
+      for (int c = 0; c < D * 2; c += 128) prefetch_l2(q + c);
+    }
     int l_base = -32, l_page = -1;                      // pages of 32 boxes, from tile l_base on
     for (int i = w.i0; i < w.i_end && ok; ++i) {
       if (i >= l_base + (32 >> bshift)) {

@@ -96,6 +96,17 @@ SWEEP = [
     ([3000, 900, 20], 8, 4, 3, 128, 64, FP, 1, 1, 0),
     ([3000, 900, 0], 4, 1, 2, 128, 16, BF, 1, 128, 200),   # more sinks than a tile
     ([700, 64], 2, 1, 1, 64, 32, FP, 1, 5000, 3),          # a window longer than the sequences
+    # more rows a K/V head: tcgen05, groups of 128 rows and of 256
+    ([700, 0, 1, 129, 128], 34, 2, 1, 128, 16, BF, 1, 0, 0),      # 17 rows
+    ([2100, 40], 33, 1, 1, 64, 128, FP, 1, 0, 0),                 # 33 rows
+    ([900, 0, 33, 2], 40, 2, 5, 128, 64, FP, 1, 0, 0),            # 100 rows, some before position 0
+    ([900, 0, 33, 2], 40, 2, 5, 64, 256, BF, 0, 0, 0),
+    ([3000, 900, 20, 0], 24, 1, 2, 128, 16, BF, 1, 100, 5),       # 48 rows under a window
+    ([3000, 900, 20], 96, 2, 1, 64, 32, FP, 1, 1, 0),             # the diagonal alone
+    ([2000, 700], 260, 2, 1, 128, 128, BF, 1, 0, 0),              # 130 rows: 256 a group
+    ([1300, 0, 131], 160, 1, 2, 64, 16, BF, 1, 300, 200),         # 320 rows in two groups, window and sinks
+    ([270, 1], 70, 2, 8, 128, 32, FP, 0, 0, 0),                   # 280 rows
+    ([140] * 30 + [0], 68, 2, 1, 64, 16, FP, 1, 0, 0),            # more groups than ranges of a CTA's own
 ]
 
 
@@ -137,6 +148,11 @@ SHARED = [
     ([514, 513, 512, 900], 8, 8, 3, 128, 256, FP, 1, 512),  # rows inside the prefix
     ([300, 160], 32, 1, 3, 64, 32, BF, 1, 160),             # part of a tile beyond whole ones
     ([400] * 40, 16, 2, 1, 128, 16, BF, 1, 384),            # several row tiles of the prefix
+    ([300] * 5, 160, 20, 1, 64, 32, FP, 1, 256),            # 40 rows of each of 20 K/V heads
+    ([300, 0, 290] * 3, 180, 60, 2, 64, 128, BF, 1, 256),   # 60 K/V heads
+    ([300, 280], 340, 170, 12, 64, 16, FP, 1, 128),         # more groups than ranges
+    ([350, 310, 0], 60, 2, 4, 128, 16, BF, 1, 256),         # 120 rows a sequence, 360 of the prefix
+    ([150] * 600 + [0], 1, 1, 1, 64, 16, BF, 1, 128),       # more sequences than lengths kept on chip
 ]
 
 
@@ -162,32 +178,40 @@ def test_sequences_shorter_than_the_shared_prefix():
     check(q, cache, True, shared_len=640, shared_table=i32(prefix))
 
 
+# query heads over 2 K/V heads: 2, 16, 40 and 150 rows take different kernels
+HEADS = [4, 32, 80, 300]
+
+
+@pytest.mark.parametrize("H", HEADS)
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
-def test_scales(scale):
-    q, cache, _ = build([333, 40], 4, 2, 2, 64, 16, BF, seed=8)
+def test_scales(scale, H):
+    q, cache, _ = build([333, 40], H, 2, 1, 64, 16, BF, seed=8)
     check(q, cache, scale=scale, out_f32=True)
 
 
-def test_large_logits_move_the_maximum():
-    q, cache, _ = build([2000], 4, 1, 1, 128, 16, BF, seed=9, std=8.0)
+@pytest.mark.parametrize("H", HEADS)
+def test_large_logits_move_the_maximum(H):
+    q, cache, _ = build([2000], H, 2, 1, 128, 16, BF, seed=9, std=8.0)
     check(q, cache, out_f32=True)
 
 
-def test_values_that_propagate():
+@pytest.mark.parametrize("H", HEADS)
+def test_values_that_propagate(H):
     """A kept NaN row reaches the sequence that keeps it and no other."""
-    q, cache, _ = build([300, 300, 300], 4, 2, 1, 64, 16, BF, seed=10)
+    q, cache, _ = build([300, 300, 300], H, 2, 1, 64, 16, BF, seed=10)
     o0, l0 = A.decode_paged(q.cuda(), cache)
     cache.k[cache.table[1, 3], 0, 5] = float("nan")
     o, l = A.decode_paged(q.cuda(), cache)
-    assert o[1, :2].isnan().all() and l[1, :2].isnan().all()
+    assert o[1, :H // 2].isnan().all() and l[1, :H // 2].isnan().all()
     keep = torch.ones_like(l, dtype=torch.bool)
-    keep[1, :2] = False
+    keep[1, :H // 2] = False
     assert torch.equal(o[keep], o0[keep]) and torch.equal(l[keep], l0[keep])
 
 
-def test_pages_that_do_not_exist_are_not_read():
+@pytest.mark.parametrize("H", HEADS)
+def test_pages_that_do_not_exist_are_not_read(H):
     """Bad entries read as rows of zeros and are reported; the others are right."""
-    q, cache, _ = build([300, 300, 40], 4, 2, 1, 64, 16, BF, seed=11)
+    q, cache, _ = build([300, 300, 40], H, 2, 1, 64, 16, BF, seed=11)
     o0, l0 = A.decode_paged(q.cuda(), cache)
     for bad in (-1, -2 ** 31, 2 ** 31 - 1, cache.k.shape[0]):
         cache.table[1, 2] = bad
@@ -208,13 +232,15 @@ def test_lengths_that_do_not_fit_are_clamped():
     assert (o[1] == 0).all() and l[1].isneginf().all()
 
 
-def test_rows_of_the_table_behind_a_window_are_not_read():
+@pytest.mark.parametrize("H", HEADS)
+def test_rows_of_the_table_behind_a_window_are_not_read(H):
     """Pages left of every row's window may be gone from the table."""
-    q, cache, _ = build([900, 700], 4, 2, 2, 64, 16, BF, seed=13)
+    q, cache, _ = build([900, 700], H, 2, 2, 64, 16, BF, seed=13)
     a = A.decode_paged(q.cuda(), cache, window=200, n_sink=3)
     for b, n in enumerate([900, 700]):
         first = n - 2 - 200 + 1
         cache.table[b, 1:first // 16] = -1
+    cache.table[:, 60:] = 2 ** 30
     o, l = A.decode_paged(q.cuda(), cache, window=200, n_sink=3)
     torch.cuda.synchronize()
     assert A.get_status() == 0
@@ -244,8 +270,9 @@ def test_equal_inputs_give_equal_bits_and_buffers_are_used():
     assert c[1] is None and torch.equal(c[0], b[0])
 
 
-def test_withheld_loads_end_in_a_status():
-    q, cache, _ = build([3000, 100, 0], 8, 2, 1, 128, 16, BF, seed=16)
+@pytest.mark.parametrize("H", HEADS)
+def test_withheld_loads_end_in_a_status(H):
+    q, cache, _ = build([3000, 100, 0], H, 2, 1, 128, 16, BF, seed=16)
     want = A.decode_paged(q.cuda(), cache)
     before = A.set_watchdog_ns(50_000_000)
     try:
@@ -259,6 +286,72 @@ def test_withheld_loads_end_in_a_status():
     got = A.decode_paged(q.cuda(), cache)
     torch.cuda.synchronize()
     assert A.get_status() == 0 and torch.equal(got[0], want[0])
+
+
+def test_withheld_loads_of_a_shared_prefix():
+    """Both launches side by side give up, one after the other, and the next call works."""
+    q, cache, prefix = build([900] * 9, 16, 2, 1, 64, 16, BF, seed=21, shared=640)
+    kw = dict(shared_len=640, shared_table=i32(prefix))
+    want = A.decode_paged(q.cuda(), cache, **kw)
+    before = A.set_watchdog_ns(50_000_000)
+    try:
+        A.test_withhold_loads(1)
+        A.decode_paged(q.cuda(), cache, **kw)
+        torch.cuda.synchronize()
+        assert A.get_status() == A.ATTN_ERR_DEVICE_TIMEOUT
+    finally:
+        A.test_withhold_loads(0)
+        A.set_watchdog_ns(before)
+    got = A.decode_paged(q.cuda(), cache, **kw)
+    torch.cuda.synchronize()
+    assert A.get_status() == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_shared_prefix_calls_back_to_back():
+    """Steps whose launches overlap (append, prefix, own positions, merge) for many steps
+    in one captured graph equal the same steps one at a time."""
+    rng = np.random.default_rng(22)
+    B, H, Hk, d = 12, 32, 2, 64
+
+    def rows(*shape):
+        return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(BF).cuda()
+
+    cache = A.paged_cache(B, 30, 500, Hk, 16, d, BF)
+    A.pages_append(cache, rows(B, Hk, 300, d), rows(B, Hk, 300, d), i32([300] + [0] * (B - 1)))
+    A.pages_fork(cache, i32([0] * (B - 1)), i32(range(1, B)))
+    table = cache.table[0, :16].clone()
+    steps = [(rows(B, Hk, 1, d), rows(B, Hk, 1, d), rows(B, H, 1, d)) for _ in range(20)]
+    lens0, table0, refs0 = cache.lens.clone(), cache.table.clone(), cache.refs.clone()
+    pages0 = cache.k.clone(), cache.v.clone()
+
+    def run(sync):
+        outs = []
+        for kn, vn, q in steps:
+            A.pages_append(cache, kn, vn)
+            outs.append(A.decode_paged(q, cache, shared_len=256, shared_table=table))
+            if sync:
+                torch.cuda.synchronize()
+        return outs
+
+    def reset():
+        for x, y in ((cache.lens, lens0), (cache.table, table0), (cache.refs, refs0), (cache.k, pages0[0]),
+                     (cache.v, pages0[1])):
+            x.copy_(y)
+        torch.cuda.synchronize()
+
+    A.get_status()
+    want = [(o.clone(), l.clone()) for o, l in run(True)]
+    reset()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(False)
+    for _ in range(3):
+        reset()
+        g.replay()
+        torch.cuda.synchronize()
+        assert A.get_status() == 0
+        for (o, l), (o1, l1) in zip(want, got):
+            assert torch.equal(o, o1) and torch.equal(l, l1)
 
 
 def test_two_streams_with_their_own_workspaces():
