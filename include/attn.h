@@ -473,8 +473,10 @@ int attn_fwd_unit_kind(int B, int H, int H_kv, int N, int window, int alibi, int
  * ATTN_ERR_DEVICE_TIMEOUT here and returns.  The backward kernel also records
  * ATTN_ERR_CUDA, and returns before doing any work, if the dynamic shared
  * memory it was given cannot hold its 1024-byte aligned layout (a launch
- * configuration fault; its outputs are then not written).  Synchronises the
- * device.
+ * configuration fault; its outputs are then not written).  The paged cache's
+ * kernels record ATTN_ERR_INVALID_ARG for device data that cannot be right and
+ * ATTN_ERR_NO_PAGES for rows that found no page (see attn_pages_t); the first
+ * code recorded stays until it is read.  Synchronises the device.
  */
 int attn_get_status(void);
 

@@ -106,6 +106,8 @@ SWEEP = [
     ([2000, 700], 260, 2, 1, 128, 128, BF, 1, 0, 0),              # 130 rows: 256 a group
     ([1300, 0, 131], 160, 1, 2, 64, 16, BF, 1, 300, 200),         # 320 rows in two groups, window and sinks
     ([270, 1], 70, 2, 8, 128, 32, FP, 0, 0, 0),                   # 280 rows
+    ([300, 190], 2, 2, 200, 64, 16, BF, 1, 0, 0),                 # 200 new rows of one head
+    ([300, 190], 2, 2, 200, 128, 32, FP, 1, 50, 7),
     ([140] * 30 + [0], 68, 2, 1, 64, 16, FP, 1, 0, 0),            # more groups than ranges of a CTA's own
 ]
 
@@ -234,11 +236,15 @@ def test_lengths_that_do_not_fit_are_clamped():
 
 @pytest.mark.parametrize("H", HEADS)
 def test_rows_of_the_table_behind_a_window_are_not_read(H):
-    """Pages left of every row's window may be gone from the table."""
+    """What lies left of every row's window and behind the sinks may be gone: the rows
+    hold NaN, the pages are no longer in the table."""
     q, cache, _ = build([900, 700], H, 2, 2, 64, 16, BF, seed=13)
     a = A.decode_paged(q.cuda(), cache, window=200, n_sink=3)
     for b, n in enumerate([900, 700]):
         first = n - 2 - 200 + 1
+        for j in range(3, first):
+            cache.k[cache.table[b, j // 16], :, j % 16] = float("nan")
+            cache.v[cache.table[b, j // 16], :, j % 16] = float("nan")
         cache.table[b, 1:first // 16] = -1
     cache.table[:, 60:] = 2 ** 30
     o, l = A.decode_paged(q.cuda(), cache, window=200, n_sink=3)
