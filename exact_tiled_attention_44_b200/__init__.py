@@ -350,7 +350,7 @@ class PagedCache:
     All contiguous, on one device.  The tensors are read-only attributes: the
     calls change their contents, in stream order.
     """
-    __slots__ = ("_t", "_c", "_ptr", "_dev", "_need")
+    __slots__ = ("_t", "_c", "_ptr", "_dev", "_cuda", "_dtype", "_sizes", "_need")
 
     def __init__(self, k, v, table, lens, refs=None):
         if k.dim() != 4 or v.shape != k.shape:
@@ -373,7 +373,8 @@ class PagedCache:
                                k.shape[1], k.shape[2], k.shape[3], table.shape[0], table.shape[1],
                                code)
         self._ptr = ctypes.addressof(self._c)
-        self._dev = dev
+        self._dev, self._cuda, self._dtype = dev, dev.type == "cuda", k.dtype
+        self._sizes = (table.shape[0], k.shape[1], k.shape[2], k.shape[3])   # B, H_kv, page_size, d
         self._need = {}      # workspace bytes by the sizes of a call
 
     k = property(lambda self: self._t[0])
@@ -414,13 +415,15 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
     the batch, with the same result.  ``workspace``: a CUDA uint8 tensor of at least
     decode_paged_workspace_bytes(...) bytes; allocated here (torch) when
     omitted.  Returns (o [B, H, N_q, d], lse [B, H, N_q] or None)."""
-    c, dev = cache._c, cache._dev
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q [B, H, N_q, d] expected")
-    B, H, N_q, d = q.shape
-    if B != c.B or d != c.d:
-        raise ValueError(f"shape mismatch q={tuple(q.shape)}, cache of {c.B} sequences, d={c.d}")
-    if q.dtype != cache._t[0].dtype:
+    B, H, N_q, d = shape
+    cB, H_kv, page_size, cd = cache._sizes
+    dev = cache._dev
+    if B != cB or d != cd:
+        raise ValueError(f"shape mismatch q={tuple(shape)}, cache of {cB} sequences, d={cd}")
+    if q.dtype != cache._dtype:
         raise TypeError("q and the cache must share one dtype")
     if q.device != dev:
         raise ValueError("q and the cache must be on one device")
@@ -433,10 +436,10 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
     if shared_table is not None:
         if shared_len < 0:
             raise ValueError("shared_len must not be negative")
-        _expect(shared_table, "shared_table", (-(-shared_len // c.page_size),), torch.int32, dev)
+        _expect(shared_table, "shared_table", (-(-shared_len // page_size),), torch.int32, dev)
     if workspace is not None:
         _expect_workspace(workspace, dev)
-    _on_cuda(dev, "decode_paged")
+    _on_cuda(cache, "decode_paged")
     if scale is None:
         scale = _DEFAULT_SCALE.get(d) or default_scale(d)
     if out is None:
@@ -447,7 +450,7 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
         sizes = (H, N_q, shared_len)
         need = cache._need.get(sizes)
         if need is None:
-            need = cache._need[sizes] = decode_paged_workspace_bytes(B, H, c.H_kv, N_q, d, shared_len)
+            need = cache._need[sizes] = decode_paged_workspace_bytes(B, H, H_kv, N_q, d, shared_len)
         workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=dev)
     _call(dev, "attn_decode_paged", q.data_ptr(), cache._ptr, out.data_ptr(),
           lse.data_ptr() if lse is not None else None,
@@ -457,8 +460,8 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
     return out, lse
 
 
-def _on_cuda(dev, what: str):
-    if dev.type != "cuda":
+def _on_cuda(cache: PagedCache, what: str):
+    if not cache._cuda:
         raise ValueError(f"{what}() takes a CUDA cache")
 
 
@@ -506,19 +509,19 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     hold too, and updates table, lens and refs.  Sequences that the free pages
     do not suffice for stay as they are; get_status() then gives
     ATTN_ERR_NO_PAGES."""
-    c = cache._c
     dev = _managed(cache, "pages_append")
+    B, H_kv, page_size, d = cache._sizes
     n_new = k_new.shape[2] if k_new.dim() == 4 else -1
-    shape = (c.B, c.H_kv, n_new, c.d)
-    _expect(k_new, "k_new", shape, cache._t[0].dtype, dev)
-    _expect(v_new, "v_new", shape, cache._t[0].dtype, dev)
+    shape = (B, H_kv, n_new, d)
+    _expect(k_new, "k_new", shape, cache._dtype, dev)
+    _expect(v_new, "v_new", shape, cache._dtype, dev)
     if counts is not None:
         _ints(counts, "counts", dev)
-        if counts.shape[0] != c.B:
-            raise ValueError(f"counts must have {c.B} elements")
-    _on_cuda(dev, "pages_append")
+        if counts.shape[0] != B:
+            raise ValueError(f"counts must have {B} elements")
+    _on_cuda(cache, "pages_append")
     workspace = _scratch(workspace, cache, ("append", n_new),
-                         lambda: load_library().attn_pages_append_workspace_bytes(c.B, n_new, c.page_size))
+                         lambda: load_library().attn_pages_append_workspace_bytes(B, n_new, page_size))
     _call(dev, "attn_pages_append", cache._ptr, k_new.data_ptr(), v_new.data_ptr(),
           counts.data_ptr() if counts is not None else None, n_new, workspace.data_ptr(),
           workspace.numel())
@@ -529,9 +532,8 @@ def pages_trim(cache: PagedCache, new_lens: torch.Tensor | None = None,
     """Shortens sequences to at most new_lens[i] (default 0: frees them) and
     releases the pages behind (attn_pages_trim).  ``rows``: int32 row numbers;
     default rows 0, 1, ... (all of them when new_lens is None too)."""
-    c = cache._c
     dev = _managed(cache, "pages_trim")
-    n = c.B
+    n = B = cache._sizes[0]
     if rows is not None:
         _ints(rows, "rows", dev)
         n = rows.shape[0]
@@ -539,11 +541,11 @@ def pages_trim(cache: PagedCache, new_lens: torch.Tensor | None = None,
         _ints(new_lens, "new_lens", dev)
         if rows is None:
             n = new_lens.shape[0]
-            if n > c.B:
-                raise ValueError(f"new_lens has {n} elements for {c.B} sequences")
+            if n > B:
+                raise ValueError(f"new_lens has {n} elements for {B} sequences")
         elif new_lens.shape[0] != n:
             raise ValueError("new_lens and rows must be of one length")
-    _on_cuda(dev, "pages_trim")
+    _on_cuda(cache, "pages_trim")
     _call(dev, "attn_pages_trim", cache._ptr, rows.data_ptr() if rows is not None else None,
           new_lens.data_ptr() if new_lens is not None else None, n)
 
@@ -556,7 +558,7 @@ def pages_fork(cache: PagedCache, parents: torch.Tensor, children: torch.Tensor)
     _ints(children, "children", dev)
     if parents.shape != children.shape:
         raise ValueError("parents and children must be of one length")
-    _on_cuda(dev, "pages_fork")
+    _on_cuda(cache, "pages_fork")
     _call(dev, "attn_pages_fork", cache._ptr, parents.data_ptr(), children.data_ptr(),
           parents.shape[0])
 
@@ -576,7 +578,7 @@ def pages_compact(cache: PagedCache, *, table_out: torch.Tensor | None = None,
         _expect(refs_out, "refs_out", (c.n_pages,), torch.int32, dev)
     if n_live is not None:
         _expect(n_live, "n_live", (1,), torch.int32, dev)
-    _on_cuda(dev, "pages_compact")
+    _on_cuda(cache, "pages_compact")
     if n_live is None:
         n_live = torch.empty(1, dtype=torch.int32, device=dev)
     workspace = _scratch(workspace, cache, "compact",
@@ -596,7 +598,7 @@ def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor) -> None:
     _ints(dst, "dst", dev)
     if src.shape != dst.shape:
         raise ValueError("src and dst must be of one length")
-    _on_cuda(dev, "pages_copy")
+    _on_cuda(cache, "pages_copy")
     _call(dev, "attn_pages_copy", cache._ptr, src.data_ptr(), dst.data_ptr(), src.shape[0])
 
 
@@ -713,7 +715,7 @@ def _check(q, k, v):
 def _expect(t: torch.Tensor, name: str, shape, dtype, device=None):
     """Caller-provided buffers must match what the C ABI will write: it sizes
     every tensor from B, H, H_kv, N and d alone."""
-    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()
+    if (t.shape != shape or t.dtype != dtype or not t.is_contiguous()
             or (device is not None and t.device != device)):
         where = f" on {device}" if device is not None else ""
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}{where}, "
