@@ -247,7 +247,7 @@ int attn_pages_copy(const attn_pages_t* c, const int* src, const int* dst, int n
   const int chunks = static_cast<int>((page_bytes(c) + attn::PG_CHUNK - 1) / attn::PG_CHUNK);
   const long long work = static_cast<long long>(n) * 2 * chunks;
   return launch(attn::attn_pages_copy_kernel, mover_grid(st, work), attn::PG_THREADS,
-                static_cast<cudaStream_t>(stream), device_pages(c, st->status), src, dst, work, chunks);
+                static_cast<cudaStream_t>(stream), device_pages(c, st->status), src, dst, n, chunks);
 }
 
 }  // extern "C"

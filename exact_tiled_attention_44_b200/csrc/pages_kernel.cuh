@@ -4,9 +4,12 @@
 // there, so the calls need no host copy of them and can be captured.
 //
 // What bounds it: moved rows are read once and written once, so the wide
-// kernels are bound by HBM; the decisions (which page is free, which sequence
-// gets it) are integer prefix sums over the sequences and over the reference
-// counts, made by one CTA in a kernel before them and bound by L2 latency.
+// kernels are bound by HBM (600 MB of prompts written in 85 us, 1.25 GB of
+// pages compacted in 189 us: 7.0 and 6.6 TB/s, at or above a plain copy's rate);
+// the decisions (which page is free, which sequence gets it) are integer prefix
+// sums over the sequences and over the reference counts, made by one CTA in a
+// kernel before them and bound by L2 latency (6 us for 64 sequences, 9 us for 9400
+// pages).
 #pragma once
 
 #include <cstdint>
@@ -432,6 +435,43 @@ __device__ __forceinline__ void pg_move_chunk(const Pages& p, int src, int dst, 
   }
 }
 
+// Pages smaller than half a chunk: moves `first`, first + 1, ... of the lists, as many
+// as fit a chunk (`per`), K and V.  Entries with a source below 0 are skipped; a bad
+// one is reported (the compaction's plan has neither).
+__device__ __forceinline__ void pg_move_small(const Pages& p, const int* src, const int* dst, long long first,
+                                              long long n, int per) {
+  const int pv = static_cast<int>(p.page_bytes >> 4);
+  uint4 x[4];
+  uint4* to[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int v = threadIdx.x + u * PG_THREADS;
+    const int m = v / (2 * pv), in = v - m * 2 * pv;
+    to[u] = nullptr;
+    if (m < per && first + m < n) {
+      const int s = src[first + m], d = dst[first + m];
+      if (s >= 0 && pg_valid(p, s) && pg_valid(p, d)) {
+        uint8_t* base = in < pv ? p.k : p.v;
+        const int off = in < pv ? in : in - pv;
+        x[u] = __ldcs(reinterpret_cast<const uint4*>(base + static_cast<size_t>(s) * p.page_bytes) + off);
+        to[u] = reinterpret_cast<uint4*>(base + static_cast<size_t>(d) * p.page_bytes) + off;
+      } else if (s >= 0 && in == 0) {
+        pg_report(p, STATUS_INVALID);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (to[u] != nullptr) __stcs(to[u], x[u]);
+}
+
+// Moves a CTA's chunk holds: 0 where a page has half a chunk or more, and its
+// chunks are moved one by one.  Several small pages at once keep the loads in
+// flight that one of 2 KB would not (18000 such pages, 4300 moved: 26.2 us a call one at a time, 19.5 so).
+__host__ __device__ inline int pg_per_chunk(long long page_bytes) {
+  return static_cast<int>(page_bytes * 2 <= PG_CHUNK ? PG_CHUNK / (2 * page_bytes) : 0);
+}
+
 // Moves the pages of the plan and writes the renumbered table and counts.
 // The sources stay as they are (a source is never a destination), so the old
 // table still reads the same rows until its pages are handed out again.
@@ -460,6 +500,12 @@ attn_pages_compact_move(const Pages p, const CompactPlan a, int* table_out, int*
     refs_out[dst] = r;
     refs_out[src] = 0;
   }
+  const int per = pg_per_chunk(p.page_bytes);
+  if (per > 0) {
+    for (long long m = static_cast<long long>(blockIdx.x) * per; m < n_moves; m += static_cast<long long>(gridDim.x) * per)
+      pg_move_small(p, a.src, a.dst, m, n_moves, per);
+    return;
+  }
   const long long work = static_cast<long long>(n_moves) * 2 * chunks;
   for (long long w = blockIdx.x; w < work; w += gridDim.x) {
     const long long i = w / (2 * chunks);
@@ -470,9 +516,16 @@ attn_pages_compact_move(const Pages p, const CompactPlan a, int* table_out, int*
 // ------------------------------------------------------------ copy
 
 __global__ void __launch_bounds__(PG_THREADS)
-attn_pages_copy_kernel(const Pages p, const int* src, const int* dst, long long work, int chunks) {
+attn_pages_copy_kernel(const Pages p, const int* src, const int* dst, int n, int chunks) {
   grid_dependency_wait();
   grid_launch_dependents();
+  const int per = pg_per_chunk(p.page_bytes);
+  if (per > 0) {
+    for (long long m = static_cast<long long>(blockIdx.x) * per; m < n; m += static_cast<long long>(gridDim.x) * per)
+      pg_move_small(p, src, dst, m, n, per);
+    return;
+  }
+  const long long work = static_cast<long long>(n) * 2 * chunks;
   for (long long w = blockIdx.x; w < work; w += gridDim.x) {
     const long long i = w / (2 * chunks);
     const int s = src[i], d = dst[i];

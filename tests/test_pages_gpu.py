@@ -144,7 +144,7 @@ def test_fork_rules():
     x.fork([7], [6])                       # an empty parent
 
 
-@pytest.mark.parametrize("page,d,Hk,n", [(16, 64, 2, 50), (64, 128, 8, 13), (256, 128, 4, 11), (16, 16, 1, 9000)])
+@pytest.mark.parametrize("page,d,Hk,n", [(16, 64, 2, 50), (16, 64, 3, 700), (32, 32, 3, 90), (64, 128, 8, 13), (256, 128, 4, 11), (16, 16, 1, 9000)])
 def test_compact(page, d, Hk, n):
     x = Both(9, max(2, n // 6), n, Hk, page, d)
     top = page * max(1, n // 12)
@@ -181,8 +181,9 @@ def test_compact_into_a_second_table_leaves_the_first_readable():
     assert torch.equal(c.k[table[table0 >= 0].long()], k0[held])  # the new ones
 
 
-def test_copy_pages():
-    x = Both(1, 1, 12, 3, 32, 128)
+@pytest.mark.parametrize("Hk,page,d", [(3, 32, 128), (1, 16, 16), (3, 16, 32), (1, 64, 64), (2, 32, 128)])
+def test_copy_pages(Hk, page, d):
+    x = Both(1, 1, 12, Hk, page, d)
     c = x.cache
     k, v = c.k.clone(), c.v.clone()
     A.pages_copy(c, i32([1, 5, -1, 7, 3]), i32([2, 6, 0, 7, 11]))
