@@ -105,8 +105,11 @@ struct PdSeq {
   int tiles;    // 0: nothing is kept (of the sequence's own positions)
 };
 
+// Lengths, table and query rows are read through L2: a launch behind a shared
+// prefix, and the merging kernels before their wait, read them without a dependency
+// wait of their own, so no line that L1 kept from before may serve them.
 __device__ __forceinline__ int pd_len_of(const PdParams& p, int b) {
-  return min(max(p.lens[b], 0), p.max_pages << p.page_shift);
+  return min(max(__ldcg(p.lens + b), 0), p.max_pages << p.page_shift);
 }
 
 // The same, from the lengths kept in shared memory (if there are any).
@@ -141,7 +144,7 @@ __device__ __forceinline__ PdSeq pd_seq(const PdParams& p, int len) {
 __device__ __forceinline__ void pd_report_lens(const PdParams& p) {
   if (blockIdx.x != 0) return;
   for (int b = threadIdx.x & 31; b < p.B; b += 32) {
-    const int n = p.lens[b];
+    const int n = __ldcg(p.lens + b);
     if (n < 0 || n > (p.max_pages << p.page_shift)) atomicCAS(p.status, 0, -1);
   }
 }
@@ -467,7 +470,7 @@ __device__ __forceinline__ void pd_look_up(const PdParams& p, PdBatch& t, int la
     const int key = pd_key(t.w.s, t.i + j, lane % PD_WARPS);
     t.have = key < t.w.s.len && !pd_gone(p, t.w.s, key);
     if (t.have)
-      t.page = p.table[(p.prefix ? 0 : static_cast<size_t>(t.w.b) * p.max_pages) + (key >> p.page_shift)];
+      t.page = __ldcg(p.table + (p.prefix ? 0 : static_cast<size_t>(t.w.b) * p.max_pages) + (key >> p.page_shift));
   }
 }
 

@@ -123,7 +123,7 @@ __device__ void pt_tma_role(const PdParams& p, PdWalk w, const CUtensorMap* tmK,
           const int key = pd_tile_key(p, w.s, li) + (lane & (boxes - 1)) * box;
           // -1: not loaded at all; a bad entry becomes a box outside the tensor
           if (key < w.s.len && !pd_gone(p, w.s, key, box)) {
-            const int page = row[key >> p.page_shift];
+            const int page = __ldcg(row + (key >> p.page_shift));
             l_page = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages) ? page : p.n_pages;
             if (l_page == p.n_pages) atomicCAS(p.status, 0, -1);
           }
@@ -283,7 +283,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
                                                         (real ? pd_row_index(p, w, r) : 0) * D);
 #pragma unroll
       for (int u = 0; u < D / 8; ++u) {
-        uint4 x = real ? src[u] : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = real ? __ldcg(src + u) : make_uint4(0u, 0u, 0u, 0u);
         st_shared_v4(row_addr + (u / 8) * G::CHUNK_BYTES + (((u % 8) ^ (L & 7)) << 4), x.x ^ q_sign, x.y ^ q_sign,
                      x.z ^ q_sign, x.w ^ q_sign);
       }

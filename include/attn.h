@@ -280,7 +280,7 @@ typedef struct attn_pages {
  *          attn_decode_paged_workspace_bytes(...) bytes, 256-byte aligned;
  *          needs no initial contents, not to be shared by calls in flight at
  *          once
- *   N_q >= 0; (H / H_kv) * N_q <= 1024 and ceil((H / H_kv) * N_q / 16) * B * H_kv *
+ *   kv->n_pages >= 1; N_q >= 0; (H / H_kv) * N_q <= 1024 and ceil((H / H_kv) * N_q / 16) * B * H_kv *
  *   (max_pages * page_size / 64 + 1) < 2^31 (else ATTN_ERR_UNSUPPORTED); d is 64 or 128;
  *   causal, window, n_sink, scale as for attn_fwd
  *
