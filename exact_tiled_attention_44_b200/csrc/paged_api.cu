@@ -20,9 +20,10 @@ struct PagedForm {
   int weight;   // 100 cycles of an SM a tile
 };
 
-// Up to 16 rows attn_paged_kernel, whose products are of 8 rows: 8 sequences
-// of up to 8192, 16 rows, d = 128 take 50 us (with 128-row products 46), 64 of
-// up to 256 take 44 us (54).  At d = 64, where a 128-row tile's exponentials
+// Up to 16 rows attn_paged_kernel, whose products are of 8 rows, d = 128: at 4
+// rows 8 sequences of up to 8192 take 33 us (with attn_paged_tc_kernel's 128-row
+// products 42), 32 of up to 16384 186 (205), 256 of up to 256 46 (150), one of 517
+// 7.8 (12.8); at 16 rows the first 47 (46), 64 of up to 256 41 (48).  At d = 64, where a 128-row tile's exponentials
 // take longer than HBM does, up to 32 rows in two groups: 34 us (37), 17 (18);
 // at d = 128 those take 67 us (47).
 PagedForm paged_form(long long rows, int d) {
