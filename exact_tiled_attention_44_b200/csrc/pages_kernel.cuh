@@ -287,9 +287,10 @@ attn_pages_append_rows(const Pages p, const AppendPlan a, const uint8_t* k_new, 
 
 // ------------------------------------------------------------ trim
 
-// One CTA a listed row.  atomicMin on the length gives every entry of the
-// list its own interval of pages, so a row that is listed twice ends at the
-// smaller length and each of its pages is released once.
+// One CTA a listed row.  Lowering the length with a compare-and-swap gives every
+// entry of the list its own interval of pages, so a row that is listed twice ends
+// at the smaller length and each of its pages is released once.  A length that
+// cannot be right is looked at first and stays as it is, with the row's pages.
 __global__ void __launch_bounds__(128)
 attn_pages_trim_kernel(const Pages p, const int* rows, const int* new_lens) {
   __shared__ int old_s;
@@ -303,7 +304,15 @@ attn_pages_trim_kernel(const Pages p, const int* rows, const int* new_lens) {
     if (threadIdx.x == 0) pg_report(p, STATUS_INVALID);
     return;
   }
-  if (threadIdx.x == 0) old_s = atomicMin(&p.lens[b], n);
+  if (threadIdx.x == 0) {
+    int old = p.lens[b];
+    while (old > n && old <= cap) {
+      const int seen = atomicCAS(&p.lens[b], old, n);
+      if (seen == old) break;
+      old = seen;              // another entry of the list lowered it
+    }
+    old_s = old;
+  }
   __syncthreads();
   const int old = old_s;
   if (old < 0 || old > cap) {

@@ -332,7 +332,8 @@ long long attn_pages_append_workspace_bytes(int B, int n_new, int page_size);
  * attn_pages_trim -- shortens sequences and releases the pages behind them:
  * for each listed row, lens = min(lens, new_lens), and the table entries past
  * the last kept page lose their reference and become -1.  Length 0 frees the
- * sequence.
+ * sequence.  A row whose length cannot be right (negative, or past the table)
+ * keeps length, table and references, and records ATTN_ERR_INVALID_ARG.
  *   rows      device, [n] int32, or NULL for rows 0 .. n - 1; a row listed twice
  *             ends at its smallest length
  *   new_lens  device, [n] int32 >= 0, or NULL for 0

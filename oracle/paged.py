@@ -160,6 +160,9 @@ class PageBook:
                 status = -1
                 continue
             old = int(self.lens[b])
+            if not 0 <= old <= self.table.shape[1] * self.page:
+                status = -1
+                continue
             if n >= old:
                 continue
             for c in range(self.pages_of(n), self.pages_of(old)):

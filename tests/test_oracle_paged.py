@@ -84,3 +84,15 @@ def test_book_random_runs_keep_their_counts():
                 b.compact()
             b.check()
             assert (b.refs >= 0).all()
+
+
+def test_book_trim_leaves_lengths_that_cannot_be_right():
+    b = oracle.PageBook(np.zeros((6, 1, 4, 1)), np.zeros((6, 1, 4, 1)), -np.ones((2, 3), int),
+                        np.zeros(2, int), np.zeros(6, int))
+    rows = np.ones((2, 1, 12, 1))
+    assert b.append(rows, rows, [12, 5]) == 0
+    table, refs = b.table.copy(), b.refs.copy()
+    for bad in (13, 2 ** 31 - 1, -1):
+        b.lens[0] = bad
+        assert b.trim([0, 4], [0, 0]) == -1 and b.lens[0] == bad
+        assert (b.table == table).all() and (b.refs == refs).all()

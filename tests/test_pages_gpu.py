@@ -251,3 +251,21 @@ def test_replayed_from_a_graph_and_on_another_stream():
         x.book.fork([0, 2], [1, 3])
         x.book.append(x.bits(kn), x.bits(vn), [0, 1, 0, 1])
     x.same()
+
+
+@pytest.mark.parametrize("over", [1, 17, 2 ** 31 - 1])
+@pytest.mark.parametrize("rows", [[1], [1, 1], [0, 1, 1, 2]])
+def test_trim_leaves_a_row_whose_length_cannot_be_right(rows, over):
+    """A length past the table (or below 0) stays, with the row's pages and their counts,
+    however often the row is listed; the other rows are trimmed."""
+    x = Both(4, 3, 20)
+    x.append(48, [48, 48, 20, 5])
+    for bad in (min(48 + over, 2 ** 31 - 1), -over):
+        x.cache.lens[1] = bad
+        x.book.lens[1] = bad
+        x.trim([17 - i for i in range(len(rows))], rows)
+        assert x.book.lens[1] == bad
+    x.cache.lens[1] = 48
+    x.book.lens[1] = 48
+    x.trim()
+    assert (x.book.refs == 0).all()
