@@ -926,11 +926,14 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           o.z = fmaf(wt, y.z, o.z);
           o.w = fmaf(wt, y.w, o.w);
         }
-        const float inv = l_exact == 0.f ? 0.f : __fdividef(1.f, l_round);
-        o.x *= inv;
-        o.y *= inv;
-        o.z *= inv;
-        o.w *= inv;
+        // a row without weights is set to 0 and not multiplied by it: its sums hold
+        // 0 times every V row that another row of the group keeps, NaN if one is not finite
+        const bool empty = l_exact == 0.f;
+        const float inv = __fdividef(1.f, l_round);
+        o.x = empty ? 0.f : o.x * inv;
+        o.y = empty ? 0.f : o.y * inv;
+        o.z = empty ? 0.f : o.z * inv;
+        o.w = empty ? 0.f : o.w * inv;
         const size_t at = (row + r) * D + c4 * 4;
         if (!direct)
           *reinterpret_cast<float4*>(po + at) = o;
@@ -940,7 +943,7 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
               make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
         if (c4 == 0) {
-          const float z = l_exact == 0.f ? -INFINITY : (top + __log2f(l_exact)) * 0.69314718055994531f;
+          const float z = empty ? -INFINITY : (top + __log2f(l_exact)) * 0.69314718055994531f;
           if (!direct) pl[row + r] = z;
           else if (p.lse != nullptr) p.lse[row + r] = z;
         }
@@ -1078,11 +1081,11 @@ __device__ __forceinline__ void pd_join(PdMix& x, PdMix y) {
 template <int D, bool BF16, bool OUT_F32>
 __device__ __forceinline__ void pd_write_mix(const PdParams& p, size_t idx, int c4, PdMix x) {
   const bool none = x.top == -INFINITY;
-  const float inv = none ? 0.f : __fdividef(1.f, x.tot);
-  x.r.x *= inv;
-  x.r.y *= inv;
-  x.r.z *= inv;
-  x.r.w *= inv;
+  const float inv = __fdividef(1.f, x.tot);
+  x.r.x = none ? 0.f : x.r.x * inv;
+  x.r.y = none ? 0.f : x.r.y * inv;
+  x.r.z = none ? 0.f : x.r.z * inv;
+  x.r.w = none ? 0.f : x.r.w * inv;
   if constexpr (OUT_F32) {
     reinterpret_cast<float4*>(static_cast<float*>(p.o) + idx * D)[c4] = x.r;
   } else {

@@ -289,7 +289,8 @@ typedef struct attn_pages {
  * or a row before position 0 under causal) gets O = 0 and LSE = -inf.  Rows of
  * the cache that no query row of the sequence keeps are never used, whatever
  * they hold; a non-finite V row that some query row keeps may also reach the other
- * rows of the same sequence (of the batch, in a shared prefix) and K/V head.  A page number outside [0, n_pages)
+ * rows of the same sequence (of the batch, in a shared prefix) and K/V head that
+ * keep any position.  A page number outside [0, n_pages)
  * reads as rows of zeros, and a length past the table's counts as the table's; both
  * record ATTN_ERR_INVALID_ARG in the status word.  Deterministic: equal inputs
  * give bitwise-equal outputs.

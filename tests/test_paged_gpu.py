@@ -210,6 +210,27 @@ def test_values_that_propagate(H):
     assert torch.equal(o[keep], o0[keep]) and torch.equal(l[keep], l0[keep])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shared", [0, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H", HEADS)
+def test_rows_that_keep_nothing_are_zero_beside_values_that_are_not_finite(H, bad, shared, d):
+    """An empty slot, and a row before position 0 whose neighbour keeps the bad V row,
+    are 0 and minus infinity exactly; with a shared prefix the bad row is every sequence's."""
+    q, cache, prefix = build([300, 200, 300], H, 2, 2, d, 16, BF, seed=23, shared=shared)
+    cache.lens.copy_(i32([300, 0, 1]))
+    kw = dict(shared_len=shared, shared_table=i32(prefix)) if shared else {}
+    cache.v[cache.table[2, 0], :, 0] = bad
+    for f32 in (False, True):
+        o, l = A.decode_paged(q.cuda(), cache, out_f32=f32, **kw)
+        torch.cuda.synchronize()
+        assert A.get_status() == 0
+        assert (o[1] == 0).all() and l[1].isneginf().all()
+        assert (o[2, :, 0] == 0).all() and l[2, :, 0].isneginf().all()
+        assert not o[2, :, 1].isfinite().any() and l[2, :, 1].isfinite().all()
+        assert o[0].isfinite().all() == (shared == 0) and l[0].isfinite().all()
+
+
 @pytest.mark.parametrize("H", HEADS)
 def test_pages_that_do_not_exist_are_not_read(H):
     """Bad entries read as rows of zeros and are reported; the others are right."""
