@@ -649,11 +649,12 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   // Fragments: lane 4 g + t holds positions g and g + 8 (of K's slice) or
   // columns g and g + 8 (of V's 16), and query rows 8 n + 2 t and 8 n + 2 t + 1.
   const int g = lane >> 2, t = lane & 3;
-  // A scale of 0 (every kept logit 0) is run as 1e-30: the logits then stay
-  // within 1e-25 of 0, every weight rounds to exactly 1 in fp32 as for 0.  A
-  // negative scale turns the signs of Q.
-  const float c = p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1e-30f;
+  // A scale of 0 (every kept logit 0, whatever the size of q . k) is run as 1
+  // with Q as zeros: the maximum is then taken of real logits, not of 0 times the
+  // minus infinity of masked ones.  A negative scale turns the signs of Q.
+  const float c = p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
   const uint32_t q_sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+  const uint32_t q_keep = p.scale_log2 != 0.f ? 0xffffffffu : 0u;
   // ldmatrix: lane -> row lane & 7 of 8 x 8 matrix lane / 8.  K: matrices
   // (positions 0-7, d 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15); V,
   // transposed: (0-7, 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15).  The four
@@ -689,10 +690,10 @@ attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       for (int n = 0; n < NT; ++n) {
         uint32_t x[4];
         pd_ldsm(q_tile + (n * 8 + mr) * T::Q_LD + (4 * k + mat) * 16, x);
-        qf[2 * k][n][0] = x[0] ^ q_sign;
-        qf[2 * k][n][1] = x[1] ^ q_sign;
-        qf[2 * k + 1][n][0] = x[2] ^ q_sign;
-        qf[2 * k + 1][n][1] = x[3] ^ q_sign;
+        qf[2 * k][n][0] = (x[0] & q_keep) ^ q_sign;
+        qf[2 * k][n][1] = (x[1] & q_keep) ^ q_sign;
+        qf[2 * k + 1][n][0] = (x[2] & q_keep) ^ q_sign;
+        qf[2 * k + 1][n][1] = (x[3] & q_keep) ^ q_sign;
       }
     __syncwarp();
     if (lane == 0) mbar_arrive(q_empty);

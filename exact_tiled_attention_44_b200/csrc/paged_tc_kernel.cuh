@@ -259,9 +259,9 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
   const uint32_t s_tmem = tmem + lane_base + T::S_COL0 + h * PT_TILE;
   const int L = wq * 32 + lane;                         // TMEM lane
   const int r = 4 * lane + wq + (PAIR ? h * 128 : 0);   // row of the group
-  // A scale of 0 is run as 1e-30 and a negative one by the signs of Q (see
-  // attn_paged_kernel)
-  const float c = p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1e-30f;
+  // A scale of 0 is run as 1 with Q as zeros, a negative one by the signs of Q
+  // (see attn_paged_kernel)
+  const float c = p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
   const uint32_t q_sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
   float* stat = reinterpret_cast<float*>(smem + T::STAT_OFF);
   uint32_t it = 0, s_ph = 0, o_ph[2] = {0, 0}, half_ph = 0;
@@ -283,7 +283,7 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, i
                                                         (real ? pd_row_index(p, w, r) : 0) * D);
 #pragma unroll
       for (int u = 0; u < D / 8; ++u) {
-        const uint4 x = real ? __ldcg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = real && p.scale_log2 != 0.f ? __ldcg(src + u) : make_uint4(0u, 0u, 0u, 0u);
         st_shared_v4(row_addr + (u / 8) * G::CHUNK_BYTES + (((u % 8) ^ (L & 7)) << 4), x.x ^ q_sign, x.y ^ q_sign,
                      x.z ^ q_sign, x.w ^ q_sign);
       }

@@ -192,6 +192,16 @@ def test_scales(scale, H):
 
 
 @pytest.mark.parametrize("H", HEADS)
+def test_scale_zero_with_large_products(H):
+    """Products of 1e30 times a scale of 0 are 0: every kept row weighs the same, and
+    LSE is the logarithm of their number."""
+    q, cache, prefix = build([333, 200], H, 2, 1, 64, 16, BF, seed=24, std=1e18, shared=128)
+    q = q * 1e12
+    check(q, cache, scale=0.0, out_f32=True)
+    check(q, cache, scale=0.0, out_f32=True, shared_len=128, shared_table=i32(prefix))
+
+
+@pytest.mark.parametrize("H", HEADS)
 def test_large_logits_move_the_maximum(H):
     q, cache, _ = build([2000], H, 2, 1, 128, 16, BF, seed=9, std=8.0)
     check(q, cache, out_f32=True)
