@@ -280,7 +280,8 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   place(dp, pl.form, pl.own);
   attn::PdParams pre = dp;
   // whole tiles of the prefix are attended once; a window moves with each
-  // row, so under one every sequence reads its own pages
+  // row, so under one (that masks anything: see dp.window) every sequence reads
+  // its own pages
   const int units = static_cast<int>((shared_len < cap ? shared_len : cap) / kSharedUnit);
   const bool shared = units > 0 && dp.window == 0;
   if (shared) {

@@ -273,16 +273,18 @@ typedef struct attn_pages {
  *          Whole tiles of them are then attended once for the query rows
  *          of all sequences instead of once a sequence.  It changes what is
  *          read, not what is computed: the result is that of shared_len = 0,
- *          up to rounding.  0 and NULL: nothing is shared.  With window > 0
- *          every sequence reads its own pages.  `table` lists all of a
- *          sequence's pages, the shared ones too.
+ *          up to rounding.  0 and NULL: nothing is shared.  Under a window
+ *          every sequence reads its own pages: the bits are those of shared_len
+ *          = 0.  `table` lists all of a sequence's pages, the shared ones too.
  *   workspace, workspace_bytes   device scratch of at least
  *          attn_decode_paged_workspace_bytes(...) bytes, 256-byte aligned;
  *          needs no initial contents, not to be shared by calls in flight at
  *          once
  *   kv->n_pages >= 1; N_q >= 0; (H / H_kv) * N_q <= 1024 and ceil((H / H_kv) * N_q / 16) * B * H_kv *
  *   (max_pages * page_size / 64 + 1) < 2^31 (else ATTN_ERR_UNSUPPORTED); d is 64 or 128;
- *   causal, window, n_sink, scale as for attn_fwd
+ *   causal, window, n_sink, scale as for attn_fwd.  A window of at least
+ *          max_pages * page_size masks nothing, and is the same as 0 in every
+ *          respect (a shared prefix is attended once under it, too)
  *
  * A query row keeps key j iff j < lens[b] and the mask rule of attn_fwd holds
  * with the row's position for i.  A row that keeps nothing (an empty sequence,

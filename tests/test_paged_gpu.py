@@ -171,6 +171,24 @@ def test_shared_prefix(case, f32):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("H", [8, 64])
+def test_a_window_that_masks_nothing_is_no_window(H):
+    """At max_pages * page_size and beyond the bits are those of window 0, shared prefix or
+    not; one position less is a window, under which nothing is shared."""
+    q, cache, prefix = build([700] * 6 + [0, 321], H, 2, 2, 64, 16, FP, seed=25, shared=320, cols=44)
+    q, cap = q.cuda(), 44 * 16
+    shared = dict(shared_len=320, shared_table=i32(prefix))
+    for kw in ({}, shared):
+        want = A.decode_paged(q, cache, **kw)
+        for window, n_sink in ((cap, 0), (cap + 1, 5), (2 ** 31 - 1, 2 ** 31 - 1)):
+            got = A.decode_paged(q, cache, window=window, n_sink=n_sink, **kw)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check(q.cpu(), cache, True, cap, 5, **shared)
+    a = A.decode_paged(q, cache, window=cap - 1, **shared)
+    b = A.decode_paged(q, cache, window=cap - 1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_sequences_shorter_than_the_shared_prefix():
     """The prefix's pages are listed for the longest; short sequences use their part of it."""
     q, cache, prefix = build([900, 700, 650], 4, 2, 2, 64, 16, BF, seed=4, shared=640)
