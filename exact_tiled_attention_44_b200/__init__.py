@@ -375,7 +375,7 @@ class PagedCache:
         self._ptr = ctypes.addressof(self._c)
         self._dev, self._cuda, self._dtype = dev, dev.type == "cuda", k.dtype
         self._sizes = (table.shape[0], k.shape[1], k.shape[2], k.shape[3])   # B, H_kv, page_size, d
-        self._need = {}      # workspace bytes by the sizes of a call
+        self._need = {}      # by call: the sizes it was last made with, and their workspace bytes
 
     k = property(lambda self: self._t[0])
     v = property(lambda self: self._t[1])
@@ -447,11 +447,8 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
     if lse is None and return_lse:
         lse = q.new_empty((B, H, N_q), dtype=torch.float32)
     if workspace is None:
-        sizes = (H, N_q, shared_len)
-        need = cache._need.get(sizes)
-        if need is None:
-            need = cache._need[sizes] = decode_paged_workspace_bytes(B, H, H_kv, N_q, d, shared_len)
-        workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=dev)
+        workspace = _scratch(None, cache, "decode", (H, N_q, shared_len),
+                             lambda: decode_paged_workspace_bytes(B, H, H_kv, N_q, d, shared_len))
     _call(dev, "attn_decode_paged", q.data_ptr(), cache._ptr, out.data_ptr(),
           lse.data_ptr() if lse is not None else None,
           shared_table.data_ptr() if shared_table is not None else None, shared_len,
@@ -490,15 +487,16 @@ def _ints(t: torch.Tensor, name: str, dev):
         raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on {dev}")
 
 
-def _scratch(workspace, cache: PagedCache, sizes, query):
-    """The caller's workspace, or one of the bytes that query() asks for."""
+def _scratch(workspace, cache: PagedCache, call: str, sizes, query):
+    """The caller's workspace, or one of the bytes that query() asks for.  The cache
+    remembers those of the last sizes of each call, not of every length it has seen."""
     if workspace is not None:
         _expect_workspace(workspace, cache._dev)
         return workspace
-    need = cache._need.get(sizes)
-    if need is None:
-        need = cache._need[sizes] = max(int(query()), 16)
-    return torch.empty(need, dtype=torch.uint8, device=cache._dev)
+    last = cache._need.get(call)
+    if last is None or last[0] != sizes:
+        last = cache._need[call] = (sizes, max(int(query()), 16))
+    return torch.empty(last[1], dtype=torch.uint8, device=cache._dev)
 
 
 def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -520,7 +518,7 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
         if counts.shape[0] != B:
             raise ValueError(f"counts must have {B} elements")
     _on_cuda(cache, "pages_append")
-    workspace = _scratch(workspace, cache, ("append", n_new),
+    workspace = _scratch(workspace, cache, "append", n_new,
                          lambda: load_library().attn_pages_append_workspace_bytes(B, n_new, page_size))
     _call(dev, "attn_pages_append", cache._ptr, k_new.data_ptr(), v_new.data_ptr(),
           counts.data_ptr() if counts is not None else None, n_new, workspace.data_ptr(),
@@ -581,7 +579,7 @@ def pages_compact(cache: PagedCache, *, table_out: torch.Tensor | None = None,
     _on_cuda(cache, "pages_compact")
     if n_live is None:
         n_live = torch.empty(1, dtype=torch.int32, device=dev)
-    workspace = _scratch(workspace, cache, "compact",
+    workspace = _scratch(workspace, cache, "compact", None,
                          lambda: load_library().attn_pages_compact_workspace_bytes(c.n_pages))
     _call(dev, "attn_pages_compact", cache._ptr,
           table_out.data_ptr() if table_out is not None else None,

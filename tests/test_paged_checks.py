@@ -199,3 +199,25 @@ def test_other_management_refusals():
     assert compact(p, None, None, 3 * M, 6 * M, M, None) == INV
     bad = struct(refs=None)
     assert compact(ctypes.addressof(bad), None, None, None, 6 * M, M, None) == INV
+
+
+def test_a_cache_remembers_one_size_of_a_call():
+    """A server's prompts and prefixes are of ever new lengths: the handle keeps the
+    workspace bytes of the last ones only, and asks again when they change."""
+    c = cpu_cache()
+    asked = []
+
+    def scratch(call, sizes, need):
+        def query():
+            asked.append(sizes)
+            return need
+        return A._scratch(None, c, call, sizes, query).numel()
+
+    for n in range(100, 200):
+        assert scratch("append", n, n) == n and scratch("append", n, n) == n
+        assert scratch("decode", (4, 1, n), 2 * n) == 2 * n and scratch("decode", (4, 1, n), 0) == 2 * n
+    assert asked == [x for n in range(100, 200) for x in (n, (4, 1, n))]
+    assert set(c._need) == {"append", "decode"}
+    assert scratch("decode", (4, 0, 0), 0) == 16 and scratch("decode", (4, -1, 0), -1) == 16
+    own = torch.zeros(7, dtype=torch.uint8)
+    assert A._scratch(own, c, "append", 1, None) is own
