@@ -229,6 +229,7 @@ def default_scale(d: int) -> float:
     return float(torch.tensor(1.0 / math.sqrt(d), dtype=torch.float32))
 
 
+_INT_MAX = 2 ** 31 - 1
 _DEFAULT_SCALE = {d: default_scale(d) for d in (64, 128)}
 
 
@@ -439,6 +440,9 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
         _expect(shared_table, "shared_table", (-(-shared_len // page_size),), torch.int32, dev)
     if workspace is not None:
         _expect_workspace(workspace, dev)
+    if not (-_INT_MAX <= window <= _INT_MAX and -_INT_MAX <= n_sink <= _INT_MAX
+            and -_INT_MAX <= shared_len <= _INT_MAX):
+        raise ValueError("window, n_sink and shared_len must fit 32 bits")   # ctypes would cut them
     _on_cuda(cache, "decode_paged")
     if scale is None:
         scale = _DEFAULT_SCALE.get(d) or default_scale(d)

@@ -221,3 +221,13 @@ def test_a_cache_remembers_one_size_of_a_call():
     assert scratch("decode", (4, 0, 0), 0) == 16 and scratch("decode", (4, -1, 0), -1) == 16
     own = torch.zeros(7, dtype=torch.uint8)
     assert A._scratch(own, c, "append", 1, None) is own
+
+
+@pytest.mark.parametrize("name", ["window", "n_sink", "shared_len"])
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63, -2 ** 31, -2 ** 32 + 5])
+def test_sizes_beyond_32_bits_are_refused(name, value):
+    """ctypes keeps the lowest 32 bits of an int: 2^32 + 5 would be a window of 5."""
+    with pytest.raises(ValueError, match="32 bits"):
+        A.decode_paged(torch.zeros(3, 4, 2, 64, dtype=BF), cpu_cache(), **{name: value})
+    with pytest.raises(ValueError, match="CUDA"):
+        A.decode_paged(torch.zeros(3, 4, 2, 64, dtype=BF), cpu_cache(), **{name: 2 ** 31 - 1})
