@@ -8,6 +8,13 @@ namespace attn_host {
 namespace {
 
 constexpr int kPagedMaxRows = 1024;   // (H / H_kv) * N_q
+
+// Whether the kernels are built for d, and the rows of a K/V head and of the
+// batch are within their limits (H a multiple of H_kv, nothing negative).
+bool paged_sizes_taken(int B, int H, int H_kv, int N_q, int d) {
+  const long long R = static_cast<long long>(H / H_kv) * N_q;
+  return (d == 64 || d == 128) && R <= kPagedMaxRows && B * R <= INT32_MAX / 2 / H_kv;
+}
 constexpr int kSharedUnit = 128;      // the shared prefix is attended in whole tiles of this many positions
 
 // How the `rows` query rows of a sequence (or, in a shared prefix, of the
@@ -191,7 +198,7 @@ extern "C" {
 long long attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int N_q, int d, int shared_len) {
   if (B < 0 || H < 0 || H_kv < 1 || N_q < 0 || d <= 0 || shared_len < 0) return -1;
   if (B == 0 || H == 0 || N_q == 0) return 0;
-  if (H % H_kv != 0) return -1;
+  if (H % H_kv != 0 || !paged_sizes_taken(B, H, H_kv, N_q, d)) return -1;
   return static_cast<long long>(paged_plan(B, H, H_kv, N_q, d, shared_len).bytes);
 }
 
@@ -206,10 +213,9 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   if (kv->B == 0 || H == 0 || N_q == 0) return ATTN_OK;
   const int B = kv->B, H_kv = kv->H_kv, d = kv->d;
   if (H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (window > 0 && !causal) return ATTN_ERR_UNSUPPORTED;
+  if (!paged_sizes_taken(B, H, H_kv, N_q, d)) return ATTN_ERR_UNSUPPORTED;
   const long long R = static_cast<long long>(H / H_kv) * N_q;
-  if (R > kPagedMaxRows || static_cast<long long>(B) * H * N_q > INT32_MAX / 2) return ATTN_ERR_UNSUPPORTED;
   // the tiles of all groups are counted in 32 bits
   const long long most = static_cast<long long>(kv->max_pages) * kv->page_size;
   const long long tile_groups = (R + 15) / 16 * B * H_kv;

@@ -6,6 +6,12 @@
 
 namespace attn_host {
 
+namespace {
+
+bool page_size_taken(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
+
+}  // namespace
+
 int validate_pages(const attn_pages_t* c, bool need_refs) {
   if (c == nullptr) return ATTN_ERR_INVALID_ARG;
   if (c->dtype != ATTN_BF16 && c->dtype != ATTN_FP16) return ATTN_ERR_INVALID_ARG;
@@ -13,7 +19,7 @@ int validate_pages(const attn_pages_t* c, bool need_refs) {
     return ATTN_ERR_INVALID_ARG;
   if (c->d != 16 && c->d != 32 && c->d != 64 && c->d != 128) return ATTN_ERR_UNSUPPORTED;
   const int ps = c->page_size;
-  if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return ATTN_ERR_UNSUPPORTED;
+  if (!page_size_taken(ps)) return ATTN_ERR_UNSUPPORTED;
   // page * H_kv + head, and sums of two positions, are 32-bit
   if (static_cast<long long>(c->n_pages) * c->H_kv > INT32_MAX ||
       static_cast<long long>(c->max_pages) * ps > (1 << 30))
@@ -111,7 +117,8 @@ using namespace attn_host;
 extern "C" {
 
 long long attn_pages_append_workspace_bytes(int B, int n_new, int page_size) {
-  if (B < 0 || n_new < 0 || page_size <= 0) return -1;
+  if (B < 0 || n_new < 0 || !page_size_taken(page_size)) return -1;
+  if (B * max_need(n_new, page_size) > INT32_MAX) return -1;   // more pages than the call counts
   const long long ints = 6ll * B + B * max_need(n_new, page_size);
   return static_cast<long long>(round_up(static_cast<size_t>(ints) * 4, 256));
 }
@@ -126,12 +133,10 @@ int attn_pages_append(const attn_pages_t* c, const void* k_new, const void* v_ne
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(workspace) || !aligned_to(counts, 4))
     return ATTN_ERR_MISALIGNED;
   const long long need = attn_pages_append_workspace_bytes(c->B, n_new, c->page_size);
-  if (workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
   const long long bh = static_cast<long long>(c->B) * c->H_kv;
   const long long row_tiles = (static_cast<long long>(n_new) + attn::PG_ROWS - 1) / attn::PG_ROWS;
-  if (bh > INT32_MAX || bh * (row_tiles + 1) > INT32_MAX ||
-      c->B * max_need(n_new, c->page_size) > INT32_MAX)
-    return ATTN_ERR_UNSUPPORTED;
+  if (need < 0 || bh > INT32_MAX || bh * (row_tiles + 1) > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
   const size_t new_bytes = static_cast<size_t>(bh) * n_new * c->d * 2;
   if (touches(c, workspace, need) || touches(c, k_new, new_bytes) || touches(c, v_new, new_bytes) ||
       overlaps(workspace, need, k_new, new_bytes) || overlaps(workspace, need, v_new, new_bytes))

@@ -304,7 +304,7 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
 
 /* Host only: bytes of workspace attn_decode_paged needs for these sizes (it
  * depends neither on the device, the lengths nor the mask), 0 for an empty
- * problem, -1 for invalid sizes. */
+ * problem, -1 for sizes that attn_decode_paged refuses. */
 long long attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int N_q, int d, int shared_len);
 
 /*
@@ -328,7 +328,7 @@ int attn_pages_append(const attn_pages_t* cache, const void* k_new, const void* 
                       const int* counts, int n_new, void* workspace, long long workspace_bytes,
                       void* stream);
 
-/* Host only: workspace bytes of attn_pages_append (-1: invalid sizes). */
+/* Host only: workspace bytes of attn_pages_append (-1: sizes that it refuses). */
 long long attn_pages_append_workspace_bytes(int B, int n_new, int page_size);
 
 /*

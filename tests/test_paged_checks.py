@@ -231,3 +231,22 @@ def test_sizes_beyond_32_bits_are_refused(name, value):
         A.decode_paged(torch.zeros(3, 4, 2, 64, dtype=BF), cpu_cache(), **{name: value})
     with pytest.raises(ValueError, match="CUDA"):
         A.decode_paged(torch.zeros(3, 4, 2, 64, dtype=BF), cpu_cache(), **{name: 2 ** 31 - 1})
+
+
+def test_workspace_queries_refuse_what_the_calls_refuse():
+    need = A.decode_paged_workspace_bytes
+    for bad in ((3, 4, 2, 513, 64), (3, 4, 2, 1, 32), (3, 4, 2, 1, 100), (2 ** 30, 4, 2, 1, 64),
+                (2 ** 31 - 1, 2 ** 31 - 1, 1, 2 ** 31 - 1, 128)):
+        assert need(*bad) == -1 and need(*bad, 128) == -1
+    assert need(3, 4, 2, 512, 64) > 0
+    most = (2 ** 31 - 1) // 2 // 8
+    assert need(most, 8, 8, 1, 64) > 0 and need(most + 1, 8, 8, 1, 64) == -1
+    pages = A.load_library().attn_pages_append_workspace_bytes
+    for bad in ((4, 100, 8), (4, 100, 48), (4, 100, 0), (4, 100, 512), (2 ** 31 - 1, 2 ** 31 - 1, 16),
+                (2 ** 31 - 1, 1, 256)):
+        assert pages(*bad) == -1
+    assert pages(1, 2 ** 31 - 1, 16) >= 4 * (2 ** 31 // 16) and pages(0, 5, 16) == 0
+    # the call itself: refused for its size, however large the workspace
+    big = struct(B=2 ** 24, max_pages=1, table=1 << 37, lens=1 << 38, refs=1 << 39)
+    assert A.load_library().attn_pages_append(ctypes.addressof(big), 1 << 40, 1 << 41, None, 2 ** 15, 1 << 42,
+                                              1 << 40, None) == UNS
