@@ -86,7 +86,11 @@ int encode_map(CUtensorMap* map, const void* base, bool bf16, int d, int n, int 
 // Launches `kern` with programmatic stream serialisation: its CTAs may be
 // scheduled while the previous grid of the stream drains, run their set-up
 // (barriers, TMEM, descriptor prefetch) and then wait for that grid in
-// grid_dependency_wait before their first memory access.
+// grid_dependency_wait before their first access to anything that it, or what
+// ran before it, may write.  Two launches of attn_decode_paged read earlier, what
+// only launches before the previous one write, and those are complete: the
+// merging kernels the lengths, and the launch behind a shared prefix everything
+// (see attn_paged_merge and attn_paged_kernel).
 template <typename... Params, typename... Args>
 cudaError_t launch_overlapped(void (*kern)(Params...), int grid, int block, size_t smem,
                               cudaStream_t stream, Args&&... args) {

@@ -60,8 +60,8 @@ enum PtBar : int {
 constexpr int PT_TMEM_SLOT_OFF = 8 * P_COUNT;
 constexpr int PT_ABORT_OFF = PT_TMEM_SLOT_OFF + 4;
 
-// The n positions from c0 on that some row of the run's sequence (prefix: of
-// the batch) keeps: j < len, and j >= lo or j < n_sink.
+// The positions j that some row of the run's sequence (prefix: of the batch)
+// keeps: j < len, and j >= lo or j < n_sink.
 struct PtUsed {
   int len, lo;
 };
@@ -250,7 +250,7 @@ __device__ void pt_mma_role(const PdParams& p, PdWalk w, uint32_t tmem, uint32_t
 }
 
 template <int D, bool PAIR, bool BF16, bool OUT_F32>
-__device__ void pt_softmax_role(const PdParams& p, PdWalk w, const PdCut& cut, int f0, uint32_t tmem, uint8_t* smem,
+__device__ void pt_softmax_role(const PdParams& p, PdWalk w, int f0, uint32_t tmem, uint8_t* smem,
                                 uint32_t sbase, uint32_t bars, int h, int wq, int lane, int longest,
                                 volatile int* abort_flag) {
   using T = PtGeo<D, PAIR>;
@@ -573,7 +573,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   if (warp < 8) {
     regs_increase<SOFTMAX_REGS>();
     if (any)
-      pt_softmax_role<D, PAIR, BF16, OUT_F32>(p, w, cut, f0, tmem, smem, sbase, bars, warp / 4, warp % 4, lane,
+      pt_softmax_role<D, PAIR, BF16, OUT_F32>(p, w, f0, tmem, smem, sbase, bars, warp / 4, warp % 4, lane,
                                               longest, abort_flag);
     tc_fence_before_sync();
     __syncthreads();

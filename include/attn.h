@@ -295,7 +295,10 @@ typedef struct attn_pages {
  * keep any position.  A page number outside [0, n_pages)
  * reads as rows of zeros, and a length past the table's counts as the table's; both
  * record ATTN_ERR_INVALID_ARG in the status word.  Deterministic: equal inputs
- * give bitwise-equal outputs.
+ * give bitwise-equal outputs.  Two launches, or three with a shared prefix, with
+ * programmatic stream serialisation as attn_fwd's (see there): the first waits for
+ * the stream's kernel before it, and a following dependent kernel has to wait
+ * (griddepcontrol.wait) before it reads o or lse, or writes what the call reads.
  */
 int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse,
                       const int* shared_table, int shared_len, void* workspace,
