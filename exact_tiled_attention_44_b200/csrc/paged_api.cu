@@ -15,6 +15,7 @@ bool paged_sizes_taken(int B, int H, int H_kv, int N_q, int d) {
   const long long R = static_cast<long long>(H / H_kv) * N_q;
   return (d == 64 || d == 128) && R <= kPagedMaxRows && B * R <= INT32_MAX / 2 / H_kv;
 }
+
 constexpr int kSharedUnit = 128;      // the shared prefix is attended in whole tiles of this many positions
 
 // How the `rows` query rows of a sequence (or, in a shared prefix, of the
@@ -30,17 +31,45 @@ struct PagedForm {
 // Up to 16 rows attn_paged_kernel, whose products are of 8 rows, d = 128: at 4
 // rows 8 sequences of up to 8192 take 33 us (with attn_paged_tc_kernel's 128-row
 // products 42), 32 of up to 16384 186 (205), 256 of up to 256 46 (150), one of 517
-// 7.8 (12.8); at 16 rows the first 47 (46), 64 of up to 256 41 (48).  At d = 64, where a 128-row tile's exponentials
-// take longer than HBM does, up to 32 rows in two groups: 34 us (37), 17 (18);
-// at d = 128 those take 67 us (47).
-PagedForm paged_form(long long rows, int d) {
+// 7.8 (12.8); at 16 rows the first 47 (46), 64 of up to 256 41 (48).
+//
+// At d = 64, where a 128-row tile's softmax takes longer than HBM does, up to 32
+// rows in two groups, unless `wide` (see paged_wide); at d = 128 two groups take 67
+// us (47).
+PagedForm paged_form(long long rows, int d, bool wide) {
   PagedForm f;
-  f.m = rows <= 8 ? 8 : rows <= (d == 64 ? 32 : 16) ? 16 : rows <= 128 ? 128 : 256;
+  f.m = rows <= 8 ? 8 : rows <= 16 || (d == 64 && rows <= 32 && !wide) ? 16 : rows <= 128 ? 128 : 256;
   f.row_tiles = static_cast<int>((rows + f.m - 1) / f.m);
   f.tile_shift = f.m <= 16 ? 6 : 7;
   f.ranges = f.m <= 16 ? 296 : 148;
   f.weight = f.m <= 16 ? 7 : f.m == 128 ? 21 : 42;
   return f;
+}
+
+// Whether, at d = 64, 17 to 32 rows are one group of attn_paged_tc_kernel and not
+// two of attn_paged_kernel.  The second group reads a sequence's tiles again when the
+// first is through with them: from L2 if the sequences are few or short, else from
+// HBM.  The lengths are on the device, so what table, window and pages allow at most
+// decides: 16384 positions a sequence, and 128 MB of K and V.  Two groups (one), us,
+// at 32 rows of each of 8 K/V heads and tables as wide as the longest sequence:
+//   65536 positions: 4 sequences 140 (112)
+//   16384: 4 sequences (93 MB) 44.7 (46.6), 8 (172 MB) 73.5 (67.4), 16 115 (108), 32 (637 MB) 223 (190)
+//   8192: 8 sequences 45.1 (46.9), 16 69.2 (69.6), 32 117 (117), 64 (630 MB) 229 (203)
+//   4096: 64 sequences 132 (131), 128 224 (222); 2000: 32 47 (57), 256 (604 MB) 230 (250)
+//   1000: 512 sequences 265 (307); 256: 64 45 (45), 256 98 (113)
+// 20 rows differ from that by 5% at most.  Short sequences in wide tables pay what
+// the 2000 and 256 show.  A prefix's length is known, and its tiles are those of one
+// sequence: of 16384 positions (34 MB) 34 us (34), 32768 47.0 (49.8), 65536 (134 MB)
+// 63.8 (55.1), 262144 197 (151).
+constexpr long long kBeyondL2 = 128ll << 20;
+
+bool paged_wide(const attn_pages_t* kv, int N_q, int window, int n_sink, int shared_len) {
+  const long long cap = static_cast<long long>(kv->max_pages) * kv->page_size;
+  const bool all_seen = window == 0 || window >= cap;
+  const long long seen = all_seen ? cap - shared_len : static_cast<long long>(window) + n_sink + N_q;
+  const long long each = seen < cap ? seen : cap, pool = static_cast<long long>(kv->n_pages) * kv->page_size;
+  const long long all = kv->B * each < pool ? kv->B * each : pool;
+  return each >= 16384 && all * kv->H_kv * kv->d * 4 >= kBeyondL2;
 }
 
 // Workspace of one attending launch over `groups` groups: two slots a range
@@ -68,15 +97,20 @@ struct PagedPlan {
   size_t bytes;
 };
 
-PagedPlan paged_plan(int B, int H, int H_kv, int N_q, int d, int shared_len) {
+PagedPlan paged_plan(int B, int H, int H_kv, int N_q, int d, int shared_len, bool wide) {
   PagedPlan pl{};
   const long long R = static_cast<long long>(H / H_kv) * N_q;
   pl.shared = shared_len >= kSharedUnit;
-  pl.form = paged_form(R, d);
-  pl.own = paged_space(0, pl.form, pl.shared ? static_cast<size_t>(B) * H_kv * pl.form.row_tiles : 0, d);
+  const auto own = [&](const PagedForm& f) {
+    return paged_space(0, f, pl.shared ? static_cast<size_t>(B) * H_kv * f.row_tiles : 0, d);
+  };
+  pl.form = paged_form(R, d, wide);
+  pl.own = own(pl.form);
+  // the workspace is sized without the table, for either form (a wide one's is no smaller)
+  pl.own.end = own(paged_form(R, d, true)).end;
   pl.bytes = pl.own.end;
   if (pl.shared) {
-    pl.prefix_form = paged_form(B * R, d);
+    pl.prefix_form = paged_form(B * R, d, 4ll * H_kv * d * shared_len >= kBeyondL2);
     pl.prefix = paged_space(pl.own.end, pl.prefix_form, static_cast<size_t>(H_kv) * pl.prefix_form.row_tiles, d);
     pl.bytes = pl.prefix.end;
   }
@@ -199,7 +233,7 @@ long long attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int N_q, int
   if (B < 0 || H < 0 || H_kv < 1 || N_q < 0 || d <= 0 || shared_len < 0) return -1;
   if (B == 0 || H == 0 || N_q == 0) return 0;
   if (H % H_kv != 0 || !paged_sizes_taken(B, H, H_kv, N_q, d)) return -1;
-  return static_cast<long long>(paged_plan(B, H, H_kv, N_q, d, shared_len).bytes);
+  return static_cast<long long>(paged_plan(B, H, H_kv, N_q, d, shared_len, false).bytes);
 }
 
 int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse, const int* shared_table,
@@ -226,7 +260,8 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   if (!aligned16(q) || !aligned16(o) || (lse != nullptr && !aligned16(lse)) ||
       !aligned_to(workspace, 256) || !aligned_to(shared_table, 4))
     return ATTN_ERR_MISALIGNED;
-  const PagedPlan pl = paged_plan(B, H, H_kv, N_q, d, shared_len);
+  const PagedPlan pl =
+      paged_plan(B, H, H_kv, N_q, d, shared_len, paged_wide(kv, N_q, window, n_sink, shared_len));
   if (static_cast<size_t>(workspace_bytes) < pl.bytes) return ATTN_ERR_INVALID_ARG;
   // no output inside an input, the workspace or another output
   const size_t rows = static_cast<size_t>(B) * H * N_q;

@@ -302,6 +302,84 @@ def test_rows_of_the_table_behind_a_window_are_not_read(H):
     assert torch.equal(o, a[0]) and torch.equal(l, a[1])
 
 
+def wide(cache, cols, n_pages):
+    """The same sequences in a wide table and a large pool, whose further pages hold NaN."""
+    big = [torch.full((n_pages, *x.shape[1:]), float("nan"), dtype=x.dtype, device="cuda") for x in (cache.k, cache.v)]
+    for x, y in zip(big, (cache.k, cache.v)):
+        x[:y.shape[0]] = y
+    table = torch.full((cache.lens.shape[0], cols), -1, dtype=torch.int32, device="cuda")
+    table[:, :cache.table.shape[1]] = cache.table
+    return A.PagedCache(*big, table, cache.lens)
+
+
+# lens, H, H_kv, N_q, page, dtype, causal, window, n_sink, shared
+WIDE = [
+    ([3000, 0, 129, 1], 40, 2, 1, 16, BF, 1, 0, 0, 0),              # 20 rows
+    ([3000, 0, 129, 3], 16, 4, 8, 64, FP, 1, 0, 0, 0),              # 32 rows, some before position 0
+    ([2000, 300] * 3, 17, 1, 1, 256, BF, 0, 0, 0, 0),
+    ([2000, 0, 300], 64, 2, 1, 16, FP, 1, 100000, 5, 0),            # a window that would see enough
+    ([2000, 0, 300], 64, 2, 1, 16, FP, 1, 200, 5, 0),               # and one that does not
+    ([900, 640, 0, 700], 64, 2, 1, 16, BF, 1, 0, 0, 640),
+    ([5, 8], 32, 1, 1, 32, BF, 1, 0, 0, 0),
+]
+
+
+@pytest.mark.parametrize("cols", [16384, 64])
+@pytest.mark.parametrize("case", WIDE, ids=[f"n{max(c[0])}H{c[1]}k{c[2]}q{c[3]}p{c[4]}w{c[7]}s{c[9]}" for c in WIDE])
+def test_17_to_32_rows_in_wide_tables(case, cols):
+    """At d = 64 these take one kernel or the other, by what the table and the pages may
+    hold; a workspace of the bytes asked for, filled before, serves both."""
+    lens, H, Hk, N_q, page, dt, causal, window, n_sink, shared = case
+    q, cache, prefix = build(lens, H, Hk, N_q, 64, page, dt, seed=26 + H, shared=shared)
+    kw = dict(shared_len=shared, shared_table=i32(prefix)) if shared else {}
+    big = wide(cache, max(cols * 16 // page, cache.table.shape[1]), (140 << 20) // (4 * 64 * Hk * page))
+    need = A.decode_paged_workspace_bytes(len(lens), H, Hk, N_q, 64, shared)
+    got = []
+    for _ in range(2):
+        ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        A.get_status()
+        got.append(A.decode_paged(q.cuda(), big, causal=bool(causal), window=window, n_sink=n_sink, workspace=ws, **kw))
+        torch.cuda.synchronize()
+        assert A.get_status() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    check(q, cache, bool(causal), window, n_sink, got=got[0])
+
+
+@pytest.mark.parametrize("shared", [65520, 65536, 65700])
+def test_prefix_of_17_to_32_rows_beyond_l2(shared):
+    """A prefix of 128 MB (the pages it lists repeat, so few hold it) goes to one kernel,
+    a shorter one to the other.  Against float64 sums on the GPU; the bounds are the
+    oracle's, with |v_j - O| taken as |v_j| + |O| and the largest logit error for all."""
+    B, H, Hk, d, page = 2, 80, 8, 64, 16                          # 10 rows a sequence
+    rng = np.random.default_rng(27)
+    k, v = (torch.from_numpy(rng.standard_normal((40, Hk, page, d)).astype(np.float32)).to(BF).cuda() for _ in range(2))
+    pages = -(-shared // page)
+    lens = [shared + 5, shared]
+    table = i32(np.stack([rng.permutation(np.resize(np.arange(40), pages + 1)) for _ in range(2)]))
+    table[1, :pages] = table[0, :pages]
+    cache = A.PagedCache(k, v, table, i32(lens))
+    q = torch.from_numpy(rng.standard_normal((B, H, 1, d)).astype(np.float32)).to(BF).cuda()
+    A.get_status()
+    o, l = A.decode_paged(q, cache, shared_len=shared, shared_table=table[0, :pages].contiguous(), out_f32=True)
+    torch.cuda.synchronize()
+    assert A.get_status() == 0
+    scale, f, u = A.default_scale(d), 2.0 ** -24, U[BF]
+    for b, n in enumerate(lens):
+        for g in range(Hk):
+            kk, vv = (x[table[b].long(), g].reshape(-1, d)[:n].double() for x in (k, v))
+            x = q[b, 10 * g:10 * g + 10, 0].double()
+            s = scale * (x @ kk.T)
+            L = torch.logsumexp(s, 1, keepdim=True)
+            w = torch.exp(s - L)
+            O, mass = w @ vv, w @ vv.abs()
+            e = (d + 4) * f * scale * float((x.abs() @ kk.abs().T).max()) + 4 * f * float(s.abs().max()) + 4 * f
+            sums = (n + 16) * f
+            rel = (u + e) / (1 - u - e) + sums
+            assert ((o[b, 10 * g:10 * g + 10, 0] - O).abs() <= rel * (mass + O.abs())).all()
+            bound = e + sums + 4 * f * (float(s.abs().max()) + float(L.abs().max()) + 1)
+            assert ((l[b, 10 * g:10 * g + 10] - L).abs() <= bound).all()
+
+
 def test_many_sequences():
     """More sequences than the kernel has threads in a CTA, most of them empty or short."""
     rng = np.random.default_rng(14)
