@@ -25,7 +25,7 @@ constexpr int kSharedUnit = 128;      // the shared prefix is attended in whole 
 // fixed, so that the workspace can be sized without a device.
 struct PagedForm {
   int m, row_tiles, tile_shift, ranges;
-  int weight;   // 100 cycles of an SM a tile
+  int weight, own_weight;   // of a tile, in a prefix and in the launch beside it (see paged_form)
 };
 
 // Up to 16 rows attn_paged_kernel, whose products are of 8 rows, d = 128: at 4
@@ -36,13 +36,23 @@ struct PagedForm {
 // At d = 64, where a 128-row tile's softmax takes longer than HBM does, up to 32
 // rows in two groups, unless `wide` (see paged_wide); at d = 128 two groups take 67
 // us (47).
+//
+// The weights share out the SMs between a prefix and the sequences' own positions
+// (pd_prefix_ranges): 100 cycles of an SM a tile, the own ones with their share of a
+// run's fixed cost.  Swept at both d: us at 0.7, 1 and 1.5 times the own weight, for
+// the rows of a sequence and of the prefix (16384 positions):
+//   4 and 512: d = 64 89, 90, 91; d = 128 117, 117, 115
+//   4 and 96: 51, 45, 50; 70, 61, 66
+//   16 and 128: 53, 45, 48; 62, 63, 68 (at 7, as 8 rows have it: 50; 78)
+//   64 and 1024: 124, 119, 119; 155, 139, 139 (at 21, as the prefix has it: 124; 155)
 PagedForm paged_form(long long rows, int d, bool wide) {
   PagedForm f;
   f.m = rows <= 8 ? 8 : rows <= 16 || (d == 64 && rows <= 32 && !wide) ? 16 : rows <= 128 ? 128 : 256;
   f.row_tiles = static_cast<int>((rows + f.m - 1) / f.m);
   f.tile_shift = f.m <= 16 ? 6 : 7;
   f.ranges = f.m <= 16 ? 296 : 148;
-  f.weight = f.m <= 16 ? 7 : f.m == 128 ? 21 : 42;
+  f.weight = f.m <= 128 ? 21 : 42;      // a prefix of 16 rows or fewer takes all SMs
+  f.own_weight = f.m == 8 ? 7 : f.m == 16 ? (d == 64 ? 9 : 12) : f.m == 128 ? 25 : 42;
   return f;
 }
 
@@ -312,7 +322,6 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
     x.row_tiles = f.row_tiles;
     x.tile_shift = f.tile_shift;
     x.ranges = f.ranges;
-    x.weight = f.weight;
     x.part_o = reinterpret_cast<float*>(ws + s.part_o);
     x.part_lse = reinterpret_cast<float*>(ws + s.part_lse);
     x.own_o = reinterpret_cast<float*>(ws + s.own_o);
@@ -331,7 +340,8 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
     place(pre, pl.prefix_form, pl.prefix);
     pre.shared_tiles = (units * kSharedUnit) >> pre.tile_shift;
     dp.shared_tiles = (units * kSharedUnit) >> dp.tile_shift;
-    pre.own_weight = dp.weight;
+    pre.weight = pl.prefix_form.weight;
+    pre.own_weight = pl.form.own_weight;
     pre.own_groups = H_kv * dp.row_tiles;
     pre.own_tile_shift = dp.tile_shift;
     pre.own_shared_tiles = dp.shared_tiles;

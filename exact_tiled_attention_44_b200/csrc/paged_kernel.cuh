@@ -58,8 +58,8 @@ struct PdParams {
   int shared_tiles;     // whole tiles of the shared prefix
   int prefix;           // this launch attends the shared prefix
   int ranges;           // CTAs of the attending kernel
-  int weight;           // time of a tile on one SM (see pd_prefix_ranges)
-  int own_weight;       // prefix: that of the sequences' own launch,
+  int weight;           // prefix: time of a tile on one SM (see pd_prefix_ranges),
+  int own_weight;       //   that of the sequences' own launch,
   int own_groups;       //   its groups a sequence
   int own_tile_shift;   //   and its tiles
   int own_shared_tiles; //   in the prefix
@@ -202,9 +202,11 @@ __device__ __forceinline__ int pd_range_of(const PdCut& c, int f) {
 // The prefix is bound by the tensor cores and exponentials, the sequences' own
 // positions by HBM, so the two launches share the SMs: the prefix takes the
 // part of them that its work is of all (`own`: tiles of the other launch's
-// groups), the other launch's CTAs the rest.  Weights are cycles of an SM a
-// tile, in hundreds, measured at d = 128.  A prefix of few rows is bound by HBM
-// itself and takes all.
+// groups), the other launch's CTAs the rest.  Weights: see paged_form.  A short
+// prefix gets a quarter of the SMs even so: on fewer its row tiles come one after
+// another, and the launch waits for them (256 rows over 2048 positions beside 64
+// sequences of up to 8000, d = 64: 1 SM 184 us, 8 141, 18 136, 37 134, 74 136, all 143; d = 128 270,
+// 222, 215, 214, 219, 228).  A prefix of few rows is bound by HBM itself and takes all.
 __device__ __forceinline__ int pd_prefix_ranges(const PdParams& pre, int own) {
   if (pre.m <= 16) return pre.ranges;
   const long long a = static_cast<long long>(pre.shared_tiles) * pre.H_kv * pre.row_tiles * pre.weight;
