@@ -576,3 +576,32 @@ def test_captured_decoding_loop():
         torch.cuda.synchronize()
         assert A.get_status() == 0 and cache.lens.tolist() == [141 + n, 2 + n, 1 + n]
         check(q.cpu(), cache, got=(out, lse))
+
+
+@pytest.mark.parametrize("H", [80, 300])
+def test_more_sequences_than_threads_in_the_kernel_of_many_rows(H):
+    """40 and 150 rows of each of 2 K/V heads over 1000 sequences: runs begin in every
+    384 of them, behind empty ones, and long sequences lie in the last."""
+    rng = np.random.default_rng(28)
+    lens = [int(x) for x in rng.integers(0, 20, 1000)]
+    for b in (0, 383, 384, 767, 768, 999):
+        lens[b] = int(rng.integers(200, 600))
+    lens[390:700] = [0] * 310
+    q, cache, _ = build(lens, H, 2, 1, 64, 16, BF, seed=28)
+    o, l = A.decode_paged(q.cuda(), cache)
+    few = [0, 1, 383, 384, 385, 389, 390, 699, 700, 766, 767, 768, 769, 998, 999]
+    part = A.PagedCache(cache.k, cache.v, cache.table[few].contiguous(), cache.lens[few].contiguous())
+    torch.cuda.synchronize()
+    assert A.get_status() == 0
+    check(q[few], part, got=(o[few], l[few]))
+    # the others against calls of at most 250 sequences: each side is off by at most
+    # 2^-8 (sum w |v - O| + |O|), where |v| <= 6 and so |v - O| <= 12, and an LSE by 1.3e-4
+    # (|q| |k| <= 144, 620 positions); 2.1 is both sides with what is of second order
+    for b in range(0, 1000, 250):
+        part = A.PagedCache(cache.k, cache.v, cache.table[b:b + 250].contiguous(), cache.lens[b:b + 250].contiguous())
+        O, L = A.decode_paged(q[b:b + 250].cuda(), part)
+        empty = part.lens == 0
+        assert (o[b:b + 250][empty] == 0).all() and l[b:b + 250][empty].isneginf().all()
+        away = (o[b:b + 250].float() - O.float()).abs()
+        assert (away <= 2.1 * 2.0 ** -8 * (12 + O.float().abs())).all()
+        assert ((l[b:b + 250][~empty] - L[~empty]).abs() <= 2.1 * 1.3e-4).all()
