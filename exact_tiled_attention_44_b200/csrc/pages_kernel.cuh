@@ -139,10 +139,11 @@ attn_pages_append_plan(const Pages p, const AppendPlan a, const int* counts, int
         c = 0;
       } else if (c > 0 && (start & (p.page_size - 1)) != 0) {
         const int last = p.table[static_cast<size_t>(b) * p.max_pages + (start >> p.page_shift)];
-        if (!pg_valid(p, last)) {
+        const int held = pg_valid(p, last) ? p.refs[last] : 0;
+        if (held < 1) {          // no such page, or one that counts as free and may be handed out
           pg_report(p, STATUS_INVALID);
           c = 0;
-        } else if (p.refs[last] > 1) {
+        } else if (held > 1) {
           from = last;
         }
       }

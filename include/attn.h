@@ -233,7 +233,7 @@ int attn_decode_noalloc(const void* q, const void* k, const void* v, void* o, fl
  *            attn_pages_fork set them to -1).
  *   lens     device, [B] int32: positions of each sequence (0: none)
  *   refs     device, [n_pages] int32: how many table entries hold the page;
- *            0 = free.  attn_decode_paged does not read it (NULL is allowed
+ *            0 (or less) = free.  attn_decode_paged does not read it (NULL is allowed
  *            there).
  *   page_size  16, 32, 64, 128 or 256 (else ATTN_ERR_UNSUPPORTED)
  *   d        16, 32, 64 or 128 (attn_decode_paged: 64 or 128)
@@ -324,7 +324,9 @@ long long attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int N_q, int
  * too (refs > 1) gets a page with a copy of its rows first (copy on write; the
  * old page loses a reference).  When the free pages do not suffice, the first
  * sequence that cannot be served and every later one that needs a page stay
- * as they are, and ATTN_ERR_NO_PAGES is recorded in the status word.  Two
+ * as they are, and ATTN_ERR_NO_PAGES is recorded in the status word.  A sequence
+ * whose partly filled last page does not exist, or has no reference, gets nothing
+ * (ATTN_ERR_INVALID_ARG).  Two
  * launches: the decisions, then the rows.
  */
 int attn_pages_append(const attn_pages_t* cache, const void* k_new, const void* v_new,

@@ -111,7 +111,7 @@ class PageBook:
     def append(self, k_new, v_new, counts=None):
         B, n_new = k_new.shape[0], k_new.shape[2]
         refs0, status, out_of_pages = self.refs.copy(), 0, False
-        free = [int(p) for p in np.flatnonzero(refs0 == 0)]
+        free = [int(p) for p in np.flatnonzero(refs0 <= 0)]
         cap = self.table.shape[1] * self.page
         for b in range(B):
             c = n_new if counts is None else int(counts[b])
@@ -123,7 +123,7 @@ class PageBook:
                 continue
             part, col = start % self.page, start // self.page
             old = int(self.table[b, col]) if part else -1
-            if part and not 0 <= old < len(self.refs):
+            if part and (not 0 <= old < len(self.refs) or refs0[old] < 1):
                 status = -1
                 continue
             copy = part > 0 and refs0[old] > 1

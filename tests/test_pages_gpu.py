@@ -269,3 +269,16 @@ def test_trim_leaves_a_row_whose_length_cannot_be_right(rows, over):
     x.book.lens[1] = 48
     x.trim()
     assert (x.book.refs == 0).all()
+
+
+@pytest.mark.parametrize("count", [0, -3])
+def test_append_does_not_write_to_a_page_that_counts_as_free(count):
+    """A partly filled last page whose count says free could be handed to another sequence
+    in the same call; its own sequence gets nothing, the others do."""
+    x = Both(4, 3, 8)
+    x.append(20, [20, 5, 16, 0])
+    page = int(x.book.table[1, 0])
+    x.cache.refs[page] = count
+    x.book.refs[page] = count
+    x.append(6, [6, 6, 0, 0])
+    assert x.book.lens.tolist() == [26, 5, 16, 0]
