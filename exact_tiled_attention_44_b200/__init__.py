@@ -440,8 +440,8 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
         _expect(shared_table, "shared_table", (-(-shared_len // page_size),), torch.int32, dev)
     if workspace is not None:
         _expect_workspace(workspace, dev)
-    if not (-_INT_MAX <= window <= _INT_MAX and -_INT_MAX <= n_sink <= _INT_MAX
-            and -_INT_MAX <= shared_len <= _INT_MAX):
+    if not -_INT_MAX <= window <= _INT_MAX or (shared_len or n_sink) and not (
+            -_INT_MAX <= n_sink <= _INT_MAX and -_INT_MAX <= shared_len <= _INT_MAX):
         raise ValueError("window, n_sink and shared_len must fit 32 bits")   # ctypes would cut them
     _on_cuda(cache, "decode_paged")
     if scale is None:
@@ -451,8 +451,11 @@ def decode_paged(q: torch.Tensor, cache: PagedCache, *, causal: bool = True, win
     if lse is None and return_lse:
         lse = q.new_empty((B, H, N_q), dtype=torch.float32)
     if workspace is None:
-        workspace = _scratch(None, cache, "decode", (H, N_q, shared_len),
-                             lambda: decode_paged_workspace_bytes(B, H, H_kv, N_q, d, shared_len))
+        last, sizes = cache._need.get("decode"), (H, N_q, shared_len)   # as _scratch, without a call
+        if last is None or last[0] != sizes:
+            need = decode_paged_workspace_bytes(B, H, H_kv, N_q, d, shared_len)
+            last = cache._need["decode"] = (sizes, max(need, 0))
+        workspace = torch.empty(last[1], dtype=torch.uint8, device=dev)
     _call(dev, "attn_decode_paged", q.data_ptr(), cache._ptr, out.data_ptr(),
           lse.data_ptr() if lse is not None else None,
           shared_table.data_ptr() if shared_table is not None else None, shared_len,
