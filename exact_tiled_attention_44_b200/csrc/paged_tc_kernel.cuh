@@ -73,6 +73,10 @@ __device__ __forceinline__ PtUsed pt_used(const PdParams& p, const PdWalk& w, in
   return u;
 }
 
+// The last kept position of a lane without a row, or whose row keeps nothing: past
+// every position, and pt_kept's hi - key0 + 1 still fits 32 bits.
+constexpr int kAllKept = INT_MAX - 1;
+
 // The lowest n bits (n <= 0: none, n >= 32: all).
 __device__ __forceinline__ uint32_t pt_low_bits(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -291,13 +295,13 @@ __device__ void pt_softmax_role(const PdParams& p, PdWalk w, int f0, uint32_t tm
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (P_Q_FULL + (PAIR ? h : 0)));
     }
-    int hi = INT_MAX, lo = 0;
+    int hi = kAllKept, lo = 0;
     if (real) pd_row_keeps(p, w, r, nullptr, hi, lo);
     // a row that keeps nothing (its sequence is empty, or it lies before
     // position 0) masks no tile; its result is set at the end
     const bool none = hi < 0;
     if (none) {
-      hi = INT_MAX;
+      hi = kAllKept;
       lo = 0;
     }
     const int hi_min = __reduce_min_sync(0xffffffffu, hi);
