@@ -31,7 +31,7 @@ struct PagedForm {
 // Up to 16 rows attn_paged_kernel, whose products are of 8 rows, d = 128: at 4
 // rows 8 sequences of up to 8192 take 33 us (with attn_paged_tc_kernel's 128-row
 // products 42), 32 of up to 16384 186 (205), 256 of up to 256 46 (150), one of 517
-// 7.8 (12.8); at 16 rows the first 47 (46), 64 of up to 256 41 (48).
+// 7.8 (12.8); at 16 rows the first 47 (46), 64 of up to 256 39 (48).
 //
 // At d = 64, where a 128-row tile's softmax takes longer than HBM does, up to 32
 // rows in two groups, unless `wide` (see paged_wide); at d = 128 two groups take 67
@@ -329,7 +329,12 @@ int attn_decode_paged(const void* q, const attn_pages_t* kv, void* o, float* lse
   };
   place(dp, pl.form, pl.own);
   attn::PdParams pre = dp;
-  // whole tiles of the prefix are attended once; a window moves with each
+  // Whole tiles of the prefix are attended once whenever the caller names one.  That
+  // costs a third launch and a merge of every row, and pays, at 4 rows of each of 8 K/V
+  // heads, 500 positions of their own and d = 128, from about 1024 positions at 32
+  // sequences on (22 us shared, 22 not; 4096: 25, 46) and at 128 (59, 62; 4096: 60,
+  // 156; 128: 59, 35); at 8 not yet at 4096 (23, 19), nor at 2 (21, 12).  The header
+  // says so, and leaves the choice to the caller.  A window moves with each
   // row, so under one (that masks anything: see dp.window) every sequence reads
   // its own pages
   const int units = static_cast<int>((shared_len < cap ? shared_len : cap) / kSharedUnit);

@@ -23,8 +23,8 @@
 // for every 128 rows (256 in PAIR) from L2.  Measured: 4180 cycles for a tile of
 // both warpgroups, of which a warpgroup's softmax takes 2400 and the products
 // behind its P 1780 (P lies over S, so the next S waits for P V); a run costs
-// 18000 cycles beside its tiles.  64 rows a K/V head, 8 sequences of up to 8192: 49
-// us; 512 rows over 16384 shared positions on all SMs: 62 us.
+// 18000 cycles beside its tiles.  64 rows a K/V head, 8 sequences of up to 8192: 54
+// us (172 MB of K and V); 512 rows over 16384 shared positions on all SMs: 62 us.
 #pragma once
 
 #include "paged_kernel.cuh"

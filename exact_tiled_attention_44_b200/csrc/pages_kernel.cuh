@@ -9,7 +9,10 @@
 // the decisions (which page is free, which sequence gets it) are integer prefix
 // sums over the sequences and over the reference counts, made by one CTA in a
 // kernel before them and bound by L2 latency (6 us for 64 sequences, 9 us for 9400
-// pages).
+// pages).  That one CTA reads 16384 counts a step, an append up to the last page it
+// needs and a compaction all of them, twice; so in a pool that is nearly full they
+// grow with it: a step of 64 sequences, appended and taken back, 8 us at 10000 pages of which
+// 95% are in use, 17 at 100000, 48 at 400000; a compaction that moves nothing 7, 30, 107.
 #pragma once
 
 #include <cstdint>

@@ -273,7 +273,9 @@ typedef struct attn_pages {
  *          Whole tiles of them are then attended once for the query rows
  *          of all sequences instead of once a sequence.  It changes what is
  *          read, not what is computed: the result is that of shared_len = 0,
- *          up to rounding.  0 and NULL: nothing is shared.  Under a window
+ *          up to rounding.  It costs a launch more, and pays from about 1024
+ *          positions at 32 sequences or more, at 8 from more than 4096; below
+ *          that shared_len = 0 is faster.  0 and NULL: nothing is shared.  Under a window
  *          every sequence reads its own pages: the bits are those of shared_len
  *          = 0.  `table` lists all of a sequence's pages, the shared ones too.
  *   workspace, workspace_bytes   device scratch of at least
