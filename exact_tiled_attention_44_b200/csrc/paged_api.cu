@@ -120,7 +120,7 @@ PagedPlan paged_plan(int B, int H, int H_kv, int N_q, int d, int shared_len, boo
   pl.own.end = own(paged_form(R, d, true)).end;
   pl.bytes = pl.own.end;
   if (pl.shared) {
-    pl.prefix_form = paged_form(B * R, d, 4ll * H_kv * d * shared_len >= kBeyondL2);
+    pl.prefix_form = paged_form(B * R, d, shared_len >= kBeyondL2 / (4ll * H_kv * d));
     pl.prefix = paged_space(pl.own.end, pl.prefix_form, static_cast<size_t>(H_kv) * pl.prefix_form.row_tiles, d);
     pl.bytes = pl.prefix.end;
   }

@@ -355,9 +355,9 @@ int attn_pages_trim(const attn_pages_t* cache, const int* rows, const int* new_l
  * attn_pages_fork -- makes row children[i] a copy of row parents[i] that shares
  * its pages (each gains a reference; no row of K or V moves).
  *   parents, children  device, [n] int32
- * A child must be empty (lens == 0), listed once, and listed as no parent; a
- * fork that breaks this is skipped (of two with one child, the first is done) and
- * records ATTN_ERR_INVALID_ARG.
+ * A child must be empty (lens == 0) and listed once, and a parent must not be
+ * listed as a child; a fork that breaks this is skipped and records
+ * ATTN_ERR_INVALID_ARG (of two with one child only the first can be done).
  */
 int attn_pages_fork(const attn_pages_t* cache, const int* parents, const int* children, int n,
                     void* stream);

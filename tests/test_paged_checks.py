@@ -250,3 +250,10 @@ def test_workspace_queries_refuse_what_the_calls_refuse():
     big = struct(B=2 ** 24, max_pages=1, table=1 << 37, lens=1 << 38, refs=1 << 39)
     assert A.load_library().attn_pages_append(ctypes.addressof(big), 1 << 40, 1 << 41, None, 2 ** 15, 1 << 42,
                                               1 << 40, None) == UNS
+
+
+def test_decode_workspace_of_the_longest_prefix():
+    """The largest prefix and the most K/V heads that the sizes allow: no overflow on the way."""
+    need, last = A.decode_paged_workspace_bytes, 2 ** 31 - 1
+    assert need(1, 2 ** 26, 2 ** 26, 1, 64, last) >= 2 * (2 ** 26) * 8 * 64 * 4
+    assert need(3, 64, 8, 1, 64, last) > need(3, 64, 8, 1, 64, 128) > need(3, 64, 8, 1, 64)
