@@ -441,6 +441,16 @@ __device__ __forceinline__ void pd_row_keeps(const PdParams& p, const PdWalk& w,
 
 // ------------------------------------------------------------ loading warp
 
+// 4-D tiled load of one box into shared memory; completes its bytes on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
 // Rows of q into shared memory: untiled copies, 16-byte aligned and a
 // multiple of 16 bytes long.
 __device__ __forceinline__ void pd_copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {

@@ -92,6 +92,20 @@ __device__ __forceinline__ uint32_t pt_kept(const PdParams& p, int key0, int hi,
 
 // ------------------------------------------------------------ roles
 
+// 5-D tiled load of one box into shared memory; completes its bytes on `bar`.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y, int z, int u, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(w)
+      : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* a) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+}
+
 template <int D, bool PAIR>
 __device__ void pt_tma_role(const PdParams& p, PdWalk w, const CUtensorMap* tmK, const CUtensorMap* tmV,
                             uint32_t sbase, uint32_t bars, int lane, volatile int* abort_flag) {

@@ -43,3 +43,16 @@ def test_traffic_figure_is_dropped_when_the_hash_differs(tmp_path, monkeypatch):
     (prof / "attn_fwd_c3_traffic.json").write_text(
         json.dumps({"kernel_src_sha256": "f" * 16, "dram_bytes_per_launch": 1.0}))
     assert b.load_traffic("c3", "fwd") == 1.0
+
+
+def test_the_hashed_header_holds_what_the_profiled_kernels_use():
+    """ptx.cuh counts as source of the forward and backward kernels: a helper there that
+    only other kernels use would turn their traffic figures off."""
+    import re
+    csrc = os.path.join(ROOT, "exact_tiled_attention_44_b200", "csrc")
+    header = open(os.path.join(csrc, "ptx.cuh")).read()
+    users = header + "".join(open(os.path.join(csrc, f)).read()
+                             for f in ("attn_kernel.cuh", "bwd_kernel.cuh", "decode_tc_kernel.cuh"))
+    names = re.findall(r"^__device__ __forceinline__ [\w ]+?[ *&](\w+)\(", header, flags=re.M)
+    assert len(names) > 20
+    assert [n for n in names if len(re.findall(rf"\b{n}\b", users)) < 2] == []
